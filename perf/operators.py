@@ -166,19 +166,22 @@ def _own(s):
 
 
 def _quantized(v, rstd, q, group):
-    """Codes and scales of v * rstd in float32: q = round(v * (Q / max|v|)), scale = rstd * max|v| / Q."""
+    """Codes and scales of v * rstd in float32: q = round(v * (Q / max|v|)), scale = rstd * max|v| / Q.
+
+    Q is a tensor in the quotients: torch takes a number over a tensor as a product with the reciprocal, which is
+    another float32 value."""
     M, N = v.shape
     top = Q_MAX[q]
     if group:
         width = -(-N // group) * group
         wide = torch.nn.functional.pad(v, (0, width - N)).view(M, width // group, group)
         most = wide.abs().amax(-1)
-        t = (wide * (top / most)[..., None]).view(M, width)[:, :N]
-        scale = rstd[:, None] * most / top
+        t = (wide * (torch.full_like(most, top) / most)[..., None]).view(M, width)[:, :N]
+        scale = rstd[:, None] * most / torch.full_like(most, top)
     else:
         most = v.abs().amax(-1)
-        t = v * (top / most)[:, None]
-        scale = rstd * most / top
+        t = v * (torch.full_like(most, top) / most)[:, None]
+        scale = rstd * most / torch.full_like(most, top)
     codes = t.to(torch.float8_e4m3fn) if q == "e4m3" else t.round().to(torch.int8)
     return codes.contiguous(), scale
 
