@@ -374,6 +374,102 @@ int gelu_bwd_host_ex(const void *dy, const void *preact, void *dx, int64_t n, in
                      size_t workspace_bytes, const gbn_options *opt, cudaStream_t stream);
 
 /*
+ * RMSNorm forward with the residual's addition, as a pre-norm block has it:
+ *   h = x + residual, rounded to dtype;  rstd = 1/sqrt(mean(h^2) + eps);
+ *   y = gamma * h * rstd.
+ * The statistics are those of the stored h, so that y and rstd are those of
+ * rms_fwd on h, and rms_add_bwd reads h.
+ *   x, residual [M,N] dtype (in), gamma [N] (in), y, h [M,N] dtype (out),
+ *   rstd [M] f32 (out).  ld_x, ld_res, ld_y, ld_h: row strides in elements,
+ *   0 for N, else >= N.  kernel: GBN_KERNEL_AUTO or GBN_KERNEL_PLAIN.
+ * y and h may each be x or residual (the same pointer and stride: the
+ * residual stream updated in place); any other overlap of an output with a
+ * row of another tensor is GBN_EINVAL.  M = 0 is a no-op.
+ */
+int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y, void *h, float *rstd, float eps,
+                int64_t M, int64_t N, int dtype, int64_t ld_x, int64_t ld_res, int64_t ld_y, int64_t ld_h, int kernel,
+                cudaStream_t stream);
+
+/*
+ * RMSNorm forward into 8 bits with scales, for a product in 8 bits:
+ * rms_fwd_q8 of x, rms_add_fwd_q8 of h = x + residual (rounded to dtype and
+ * written to h).  With v = gamma * h in float32, a = max |v| over the row
+ * (group 0) or over each 128 columns (group 128; the last group may be
+ * shorter), and Q = 448 (GBN_E4M3) or 127 (GBN_INT8):
+ *   code = round(v * (Q/a)),  scale = rstd * a / Q:  code * scale stands
+ *   for y = gamma * h * rstd.
+ * Q/a, its product with v and the scale are float32 operations, rounded to
+ * nearest even, and so is the code.  A row (group) of zeros has codes 0 and
+ * scale 0; where a row holds a NaN or an infinity, scales and e4m3 codes
+ * are NaN as y would be (int8 codes of a NaN are 0).
+ *   q [M,N] one byte each (out); scale [M] f32 (group 0) or
+ *   [M, ceil(N/128)] f32, contiguous (out); h [M,N] dtype (out); rstd [M] f32
+ *   (out); strides, kernel and overlaps as for rms_add_fwd (q overlaps no
+ *   other tensor).
+ */
+enum { GBN_E4M3 = 16, GBN_INT8 = 17 };
+int rms_fwd_q8(const void *x, const void *gamma, void *q, float *scale, float *rstd, float eps, int64_t M, int64_t N,
+               int dtype, int q_dtype, int64_t group, int64_t ld_x, int64_t ld_q, int kernel, cudaStream_t stream);
+int rms_add_fwd_q8(const void *x, const void *residual, const void *gamma, void *q, float *scale, void *h,
+                   float *rstd, float eps, int64_t M, int64_t N, int dtype, int q_dtype, int64_t group, int64_t ld_x,
+                   int64_t ld_res, int64_t ld_q, int64_t ld_h, int kernel, cudaStream_t stream);
+
+/*
+ * Backward of rms_add_fwd: with dy the gradient of y and dh the gradient
+ * that reaches h on its other way (the residual stream),
+ *   dx = rstd*(dyhat - xhat*mean(dyhat*xhat)) + dh,  xhat = h*rstd,
+ *   dgamma[j] = sum over rows of dy*xhat;
+ * dx is the gradient of x and of residual alike.  The sum with dh is taken
+ * in float32 before the one rounding to dtype.
+ *   dy, dh, h [M,N] dtype (in), gamma [N] (in), rstd [M] f32 (in, required),
+ *   dx [M,N] dtype (out; may be dy, dh or h: same pointer and stride, any
+ *   other overlap is GBN_EINVAL), dgamma [N] (out).  ld_dh: row stride of dh
+ *   (0: N).  Of opt (may be NULL) ld_x (of h), ld_dy, ld_out (of dx),
+ *   accumulate, grad_dtype, kernel and wait_limit_ns apply; the others must
+ *   be zero.  workspace: gbn_bwd_workspace_bytes(M, N, dtype, 0) bytes, as for
+ *   rms_bwd.
+ */
+int rms_add_bwd(const void *dy, const void *dh, const void *h, const void *gamma, const float *rstd, void *dx,
+                void *dgamma, int64_t M, int64_t N, int dtype, void *workspace, size_t workspace_bytes, int64_t ld_dh,
+                const gbn_options *opt, cudaStream_t stream);
+
+/*
+ * The global 2-norm of many gradient tensors, and their clip:
+ *   norm = sqrt(sum over tensors and elements of g^2),
+ *   coef = min(1, max_norm / (norm + eps)),  out = g * coef, rounded once.
+ * tensors: a HOST array of `count` descriptors (n contiguous elements of
+ * dtype in device memory, aligned to the element); it is read before the
+ * call returns, nothing of it is kept, and a captured call replays with the
+ * addresses it was given.  Types may be mixed.  count = 0 gives norm 0.
+ *   norm: one float32 in device memory (out).  workspace: device memory of
+ *   gbn_grad_workspace_bytes() bytes, any alignment, its contents on entry
+ *   do not matter; two calls that may run at once need one each.
+ *   Squares are summed in float32 within 64 bytes a thread and in float64
+ *   from there, in a fixed order: the same bits from run to run.  A norm
+ *   above the largest float32 is infinity.
+ *   gbn_grad_clip: out is NULL (in place) or `count` descriptors of the same
+ *   n and dtype, none of which overlaps a gradient other than its own and
+ *   that one not in part.  A tensor must not be listed twice.  A norm that is
+ *   NaN makes every output NaN, an infinite one makes finite elements zero.
+ *   max_norm >= 0, eps >= 0, neither NaN.
+ * gbn_grad_check returns GBN_EINVAL if two of the tensors share memory (or a
+ * descriptor is invalid); it needs no device.
+ */
+typedef struct {
+    void *data;
+    int64_t n;
+    int dtype;
+    int reserved; /* zero */
+} gbn_tensor;
+
+size_t gbn_grad_workspace_bytes(void);
+int gbn_grad_norm(const gbn_tensor *tensors, int64_t count, float *norm, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+int gbn_grad_clip(const gbn_tensor *tensors, const gbn_tensor *out, int64_t count, float max_norm, float eps,
+                  float *norm, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int gbn_grad_check(const gbn_tensor *tensors, int64_t count);
+
+/*
  * Every wait inside the library's kernels (on a shared-memory barrier that
  * a bulk copy completes) gives up after about two seconds; the kernel then
  * records an error code in a per-device flag, drains its own copies with

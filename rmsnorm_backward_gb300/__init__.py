@@ -28,12 +28,18 @@ __all__ = [
     "ln_bwd_host", "rms_bwd_host", "bwd_host_workspace_bytes", "silu_bwd", "gelu_bwd", "REDUCE_MODES", "KERNELS",
     "silu_bwd_host", "gelu_bwd_host",
     "device_error", "status_string", "DTYPE_CODES",
+    "rms_add_fwd", "rms_fwd_q8", "rms_add_fwd_q8", "rms_add_bwd", "Q_DTYPE_CODES", "QUANT_GROUP",
+    "GradList", "grad_norm", "grad_clip", "grad_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "_lib", "libgbnorm.so")
 
 DTYPE_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+# 8-bit output types (GBN_E4M3, GBN_INT8) and the columns that share a scale
+# where the scales are by group
+Q_DTYPE_CODES = {torch.float8_e4m3fn: 16, torch.int8: 17}
+QUANT_GROUP = 128
 GBN_OK = 0
 
 _lock = threading.Lock()
@@ -52,6 +58,12 @@ class GbnOptions(ctypes.Structure):
     _fields_ = [("ld_x", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("ld_out", ctypes.c_int64),
                 ("accumulate", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("reduce_mode", ctypes.c_int),
                 ("kernel", ctypes.c_int), ("host_chunk", ctypes.c_int64), ("wait_limit_ns", ctypes.c_int64)]
+
+
+class _GbnTensor(ctypes.Structure):
+    """gbn_tensor of include/gbnorm.h."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int)]
 
 
 # reduce_mode values (GBN_REDUCE_* of include/gbnorm.h)
@@ -103,6 +115,15 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gelu_bwd_host.argtypes = [_vp, _vp, _vp, _i64, _int, _vp, _sz, _vp]
     L.silu_bwd.argtypes = [_vp, _vp, _vp, _i64, _int, _vp]
     L.gelu_bwd.argtypes = [_vp, _vp, _vp, _i64, _int, _vp]
+    L.rms_add_fwd.argtypes = [_vp] * 6 + [_f, _i64, _i64, _int] + [_i64] * 4 + [_int, _vp]
+    L.rms_fwd_q8.argtypes = [_vp] * 5 + [_f, _i64, _i64, _int, _int, _i64, _i64, _i64, _int, _vp]
+    L.rms_add_fwd_q8.argtypes = [_vp] * 7 + [_f, _i64, _i64, _int, _int] + [_i64] * 5 + [_int, _vp]
+    L.rms_add_bwd.argtypes = [_vp] * 7 + [_i64, _i64, _int, _vp, _sz, _i64, opt, _vp]
+    L.gbn_grad_workspace_bytes.argtypes = []
+    L.gbn_grad_workspace_bytes.restype = _sz
+    L.gbn_grad_norm.argtypes = [_vp, _i64, _vp, _vp, _sz, _vp]
+    L.gbn_grad_clip.argtypes = [_vp, _vp, _i64, _f, _f, _vp, _vp, _sz, _vp]
+    L.gbn_grad_check.argtypes = [_vp, _i64]
     L.gbn_device_error.argtypes = [_int]
     L.gbn_status_string.argtypes = [_int]
     L.gbn_status_string.restype = ctypes.c_char_p
@@ -110,7 +131,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
                  "ln_bwd_rows", "rms_bwd_rows",
                  "gbn_bwd_reduce", "gbn_bwd_plan", "gbn_device_error", "silu_bwd", "gelu_bwd",
                  "ln_bwd_host", "rms_bwd_host", "silu_bwd_host", "gelu_bwd_host", "ln_bwd_host_ex",
-                 "rms_bwd_host_ex", "silu_bwd_host_ex", "gelu_bwd_host_ex"):
+                 "rms_bwd_host_ex", "silu_bwd_host_ex", "gelu_bwd_host_ex", "rms_add_fwd", "rms_fwd_q8",
+                 "rms_add_fwd_q8", "rms_add_bwd", "gbn_grad_norm", "gbn_grad_clip", "gbn_grad_check"):
         getattr(L, name).restype = _int
     return L
 
@@ -414,6 +436,297 @@ def silu_bwd(dy: torch.Tensor, preact: torch.Tensor, *, dx: Optional[torch.Tenso
 def gelu_bwd(dy: torch.Tensor, preact: torch.Tensor, *, dx: Optional[torch.Tensor] = None, stream=None):
     """dx = dy * GELU'(preact) (exact erf form), elementwise; ``dx`` may be ``dy``."""
     return _act_bwd("gelu_bwd", dy, preact, dx, stream)
+
+
+# ---------------------------------------------------------------------------
+# RMSNorm with the residual's addition and / or an 8-bit output, its backward
+# ---------------------------------------------------------------------------
+_ROW_KERNELS = {"auto": 0, "plain": 2}
+
+
+def _enqueue(fn: str, device, stream, args, owned=()) -> None:
+    """Calls the library's ``fn(*args, stream)`` with ``device`` current.
+    owned: tensors allocated for this call; where it runs on another stream
+    than the one they were allocated on, their memory stays theirs until that
+    stream is done with it."""
+    call = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        status = call(*args, _stream(device, stream))
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, _stream(device, stream))
+    if status != GBN_OK:
+        raise GbnError(fn, status)
+    if stream is not None and owned:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        for t in owned:
+            t.record_stream(stream)
+
+
+def _out_rows(t: Optional[torch.Tensor], name: str, shape, dtype, device, owned) -> Tuple[torch.Tensor, int]:
+    """An output of ``shape`` (allocated if None) and its row stride."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        owned.append(t)
+        return t, shape[-1]
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t, _rows_ld(t, name)[2]
+
+
+def _out_vec(t: Optional[torch.Tensor], name: str, n: int, device, owned) -> torch.Tensor:
+    if t is None:
+        t = torch.empty(n, dtype=torch.float32, device=device)
+        owned.append(t)
+    else:
+        _vec(t, name, n, torch.float32, device)
+    return t
+
+
+def rms_add_fwd(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, eps: float, *,
+                y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                rstd: Optional[torch.Tensor] = None, kernel: str = "auto", stream=None):
+    """RMSNorm of ``x + residual`` over the last dimension. Returns (y, h, rstd).
+
+    h is the sum, rounded to x's dtype: the residual stream that goes on, and
+    what rms_add_bwd reads.  y and h may each be x or residual (in place).
+    Row tensors may be 2-D views with contiguous rows.  kernel: "auto" or
+    "plain"."""
+    M, N, ld_x = _rows_ld(x, "x")
+    device, owned = x.device, []
+    ld_r = _same_rows(residual, x, "residual")
+    _vec(gamma, "gamma", N, x.dtype, device)
+    y, ld_y = _out_rows(y, "y", x.shape, x.dtype, device, owned)
+    h, ld_h = _out_rows(h, "h", x.shape, x.dtype, device, owned)
+    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    _enqueue("rms_add_fwd", device, stream,
+             (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), y.data_ptr(), h.data_ptr(), rstd.data_ptr(),
+              eps, M, N, _code(x), ld_x, ld_r, ld_y, ld_h, _ROW_KERNELS[kernel]), owned)
+    return y, h, rstd
+
+
+def _q8_args(x, N, q_dtype, group, q, scale, M, owned):
+    if q is not None:
+        q_dtype = q.dtype
+    if q_dtype not in Q_DTYPE_CODES:
+        raise ValueError(f"q_dtype must be one of {sorted(map(str, Q_DTYPE_CODES))}")
+    if group not in (0, QUANT_GROUP):
+        raise ValueError(f"group must be 0 (a scale for each row) or {QUANT_GROUP}")
+    q, ld_q = _out_rows(q, "q", x.shape, q_dtype, x.device, owned)
+    shape = x.shape[:-1] + ((N + QUANT_GROUP - 1) // QUANT_GROUP,) if group else x.shape[:-1]
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        owned.append(scale)
+    elif scale.dtype != torch.float32 or scale.shape != shape or not scale.is_contiguous() or scale.device != x.device:
+        raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(shape)} on {x.device}")
+    return q, ld_q, scale, Q_DTYPE_CODES[q_dtype]
+
+
+def rms_fwd_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, q_dtype=torch.float8_e4m3fn, group: int = 0,
+               q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+               rstd: Optional[torch.Tensor] = None, kernel: str = "auto", stream=None):
+    """RMSNorm of x into 8 bits with scales. Returns (q, scale, rstd).
+
+    q (float8_e4m3fn or int8) times scale stands for gamma * x * rstd.
+    group 0: a scale for each row, shape x.shape[:-1]; group 128: a scale for
+    each 128 columns, shape x.shape[:-1] + (ceil(N / 128),).  A given q decides
+    q_dtype.  kernel: "auto" or "plain"."""
+    M, N, ld_x = _rows_ld(x, "x")
+    device, owned = x.device, []
+    _vec(gamma, "gamma", N, x.dtype, device)
+    q, ld_q, scale, q_code = _q8_args(x, N, q_dtype, group, q, scale, M, owned)
+    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    _enqueue("rms_fwd_q8", device, stream,
+             (x.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), eps, M, N, _code(x),
+              q_code, group, ld_x, ld_q, _ROW_KERNELS[kernel]), owned)
+    return q, scale, rstd
+
+
+def rms_add_fwd_q8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, eps: float, *,
+                   q_dtype=torch.float8_e4m3fn, group: int = 0, q: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, kernel: str = "auto", stream=None):
+    """RMSNorm of ``x + residual`` into 8 bits with scales. Returns (q, scale, h, rstd).
+
+    h as in rms_add_fwd (it may be x or residual), the rest as in rms_fwd_q8."""
+    M, N, ld_x = _rows_ld(x, "x")
+    device, owned = x.device, []
+    ld_r = _same_rows(residual, x, "residual")
+    _vec(gamma, "gamma", N, x.dtype, device)
+    q, ld_q, scale, q_code = _q8_args(x, N, q_dtype, group, q, scale, M, owned)
+    h, ld_h = _out_rows(h, "h", x.shape, x.dtype, device, owned)
+    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    _enqueue("rms_add_fwd_q8", device, stream,
+             (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), h.data_ptr(),
+              rstd.data_ptr(), eps, M, N, _code(x), q_code, group, ld_x, ld_r, ld_q, ld_h, _ROW_KERNELS[kernel]),
+             owned)
+    return q, scale, h, rstd
+
+
+def rms_add_bwd(dy: torch.Tensor, dh: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor, *,
+                dx=None, dgamma=None, workspace=None, accumulate: bool = False, grad_dtype=torch.float32,
+                kernel: str = "auto", stream=None):
+    """Backward of rms_add_fwd. Returns (dx, dgamma).
+
+    dy: the gradient of y; dh: the gradient that reaches h on its other way
+    (the residual stream); h, rstd: as rms_add_fwd returned them.  dx, which
+    may be dy, dh or h, is the gradient of x and of residual alike.  dgamma,
+    accumulate, grad_dtype and workspace as for rms_bwd; kernel: "auto" or
+    "plain"."""
+    if grad_dtype not in (torch.float32, h.dtype):
+        raise ValueError("grad_dtype must be float32 or h's dtype")
+    M, N, ld_h = _rows_ld(h, "h")
+    device, owned = h.device, []
+    ld_dy = _same_rows(dy, h, "dy")
+    ld_dh = _same_rows(dh, h, "dh")
+    _vec(gamma, "gamma", N, h.dtype, device)
+    _vec(rstd, "rstd", M, torch.float32, device)
+    dx, ld_dx = _out_rows(dx, "dx", h.shape, h.dtype, device, owned)
+    if dgamma is None:
+        dgamma = _grads(None, "dgamma", N, grad_dtype, device, accumulate)
+        owned.append(dgamma)
+    else:
+        _vec(dgamma, "dgamma", N, grad_dtype, device)
+    if workspace is None:
+        workspace = torch.empty(max(bwd_workspace_bytes(M, N, h.dtype, False, device), 1), dtype=torch.uint8,
+                                device=device)
+        owned.append(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on h's device")
+    opt = GbnOptions(ld_h, ld_dy, ld_dx, 1 if accumulate else 0, DTYPE_CODES[grad_dtype], 0, _ROW_KERNELS[kernel], 0, 0)
+    _enqueue("rms_add_bwd", device, stream,
+             (dy.data_ptr(), dh.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+              dgamma.data_ptr(), M, N, _code(h), workspace.data_ptr(), workspace.nbytes, ld_dh, ctypes.byref(opt)),
+             owned)
+    return dx, dgamma
+
+
+# ---------------------------------------------------------------------------
+# the global gradient norm and the clip
+# ---------------------------------------------------------------------------
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one block of memory, each place once."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+class GradList:
+    """The gradients of a program that keeps them in place: a list of float32,
+    float16 or bfloat16 tensors on one device, checked once and handed to
+    grad_norm / grad_clip again and again.
+
+    Every tensor's elements have to fill one block of memory (contiguous, or a
+    permutation of that).  The list keeps the tensors and their storages; it
+    describes the memory that they had when it was made."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        self.tensors = tensors
+        self.device = tensors[0].device if tensors else None
+        self._table = (_GbnTensor * len(tensors))()
+        for i, t in enumerate(tensors):
+            if not t.is_cuda or t.device != self.device:
+                raise ValueError("gradients must be CUDA tensors on one device")
+            if t.dtype not in DTYPE_CODES:
+                raise ValueError(f"unsupported dtype {t.dtype}")
+            if not _dense(t):
+                raise ValueError("a gradient's elements must fill one block of memory")
+            e = self._table[i]
+            e.data, e.n, e.dtype = t.data_ptr(), t.numel(), DTYPE_CODES[t.dtype]
+        self._storages = [t.untyped_storage() for t in tensors]
+        self._disjoint = None
+        self._out_of = None  # the list that this one was checked to be an output of
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def _check_apart(self):
+        if self._disjoint is None:
+            self._disjoint = lib().gbn_grad_check(self._table, len(self.tensors)) == GBN_OK
+        if not self._disjoint:
+            raise ValueError("clipped gradients must not share memory")
+
+    def _check_out_of(self, grads: "GradList"):
+        """Raises unless this list can take grads' clipped values."""
+        if self._out_of is grads:
+            return
+        if len(self) != len(grads) or (len(self) and self.device != grads.device):
+            raise ValueError("out must have a tensor for each gradient, on their device")
+        both = []
+        for o, g in zip(self.tensors, grads.tensors):
+            if o.shape != g.shape or o.dtype != g.dtype or (o.stride() != g.stride() and not
+                                                            (o.is_contiguous() and g.is_contiguous())):
+                raise ValueError("out must match the gradients in shape, dtype and layout")
+            if o.data_ptr() != g.data_ptr():
+                both.append(g)
+        both = GradList(self.tensors + both)
+        if lib().gbn_grad_check(both._table, len(both)) != GBN_OK:
+            raise ValueError("out must not share memory with another gradient or output")
+        self._out_of = grads
+
+
+def grad_workspace_bytes(device=None) -> int:
+    """Workspace bytes grad_norm and grad_clip need on ``device`` (default: current)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(lib().gbn_grad_workspace_bytes())
+
+
+def _grad_args(grads, norm, workspace, owned):
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    device = grads.device
+    if device is None:
+        device = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        owned.append(norm)
+    else:
+        _vec(norm, "norm", 1, torch.float32, device)
+    if workspace is None:
+        workspace = torch.empty(grad_workspace_bytes(device), dtype=torch.uint8, device=device)
+        owned.append(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the gradients' device")
+    return grads, norm, workspace, device
+
+
+def grad_norm(grads, *, norm: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
+    """The 2-norm of all gradients together, as a float32 tensor of no dimensions.
+
+    grads: a GradList, or tensors (a GradList is made for the call)."""
+    owned = []
+    grads, norm, workspace, device = _grad_args(grads, norm, workspace, owned)
+    _enqueue("gbn_grad_norm", device, stream,
+             (grads._table, len(grads.tensors), norm.data_ptr(), workspace.data_ptr(), workspace.nbytes), owned)
+    return norm
+
+
+def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: Optional[torch.Tensor] = None,
+              workspace=None, stream=None) -> torch.Tensor:
+    """Multiplies all gradients by min(1, max_norm / (norm + eps)), norm being
+    their 2-norm together, and returns that norm (before the clip).
+
+    grads: a GradList, or tensors (a GradList is made for the call); they are
+    clipped in place, or into ``out`` (a GradList or tensors of the same
+    shapes, types and layouts)."""
+    owned = []
+    grads, norm, workspace, device = _grad_args(grads, norm, workspace, owned)
+    grads._check_apart()
+    if out is not None:
+        if not isinstance(out, GradList):
+            out = GradList(out)
+        out._check_out_of(grads)
+    _enqueue("gbn_grad_clip", device, stream,
+             (grads._table, None if out is None else out._table, len(grads.tensors), max_norm, eps, norm.data_ptr(),
+              workspace.data_ptr(), workspace.nbytes), owned)
+    return norm
 
 
 # ---------------------------------------------------------------------------

@@ -5,13 +5,18 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "bwd_ws_layout.h"
 #include "gbn_launch.h"
 #include "gbnorm.h"
+#include "grad_clip.h"
+#include "rms_add_bwd.h"
+#include "rms_out.h"
 
 namespace gbn {
 namespace {
@@ -642,12 +647,206 @@ int act_host_impl(int act, const void *dy, const void *preact, void *dx, int64_t
     return GBN_OK;
 }
 
+// ---------------------------------------------------------------------------
+// RMSNorm with a residual's addition and / or an 8-bit output, its backward,
+// the gradient norm and the clip
+// ---------------------------------------------------------------------------
+// M rows of `row` bytes, `ld` bytes apart
+struct RowSpan {
+    const void *p;
+    int64_t ld, row;
+};
+
+bool same_rows(const RowSpan &a, const RowSpan &b) { return a.p == b.p && a.ld == b.ld && a.row == b.row; }
+
+// Whether the rows of a and of b have no byte in common.  Rows of one stride
+// that lie between one another (two halves of wider rows) are told apart;
+// spans of different strides that reach into one another count as common.
+bool apart(const RowSpan &a, const RowSpan &b, int64_t M) {
+    if (M <= 0) return true;
+    const intptr_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
+    if (pa + (M - 1) * a.ld + a.row <= pb || pb + (M - 1) * b.ld + b.row <= pa) return true;
+    if (M == 1 || a.ld != b.ld) return false;
+    intptr_t d = (pb - pa) % a.ld;
+    if (d < 0) d += a.ld;
+    return d >= a.row && d + b.row <= a.ld;
+}
+
+// an output against an input row by row: apart, or the same rows (updated in place)
+bool out_over_in(const RowSpan &out, const RowSpan &in, int64_t M) { return same_rows(out, in) || apart(out, in, M); }
+
+bool valid_eps(float eps) { return eps >= 0.f && isfinite(eps); }
+
+// kind: an OutKind; h and res both given or both null
+int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool has_res, const void *gamma, void *out,
+                 float *scale, void *h, float *rstd, float eps, int64_t M, int64_t N, int dtype, int64_t ld_x,
+                 int64_t ld_res, int64_t ld_out, int64_t ld_h, int kernel, cudaStream_t stream) {
+    int st = check_shape(M, N, dtype);
+    if (st != GBN_OK) return st;
+    if (!valid_eps(eps) || (group != 0 && group != kQuantGroup)) return GBN_EINVAL;
+    if (kernel != GBN_KERNEL_AUTO && kernel != GBN_KERNEL_PLAIN) return GBN_EINVAL;
+    if (!ld_x) ld_x = N;
+    if (!ld_res) ld_res = N;
+    if (!ld_out) ld_out = N;
+    if (!ld_h) ld_h = N;
+    if (ld_x < N || ld_res < N || ld_out < N || ld_h < N) return GBN_EINVAL;
+    if (M == 0) return GBN_OK;
+    if (!x || !gamma || !out || !rstd || (has_res && (!res || !h)) || (kind != kOutSame && !scale)) return GBN_EINVAL;
+    const int64_t es = elem_bytes(dtype), eo = kind == kOutSame ? es : 1;
+    const RowSpan sx{x, ld_x * es, N * es}, sr{res, ld_res * es, N * es}, sh{h, ld_h * es, N * es},
+        so{out, ld_out * eo, N * eo};
+    if (kind == kOutSame ? !out_over_in(so, sx, M) : !apart(so, sx, M)) return GBN_EINVAL;
+    if (has_res) {
+        if (kind == kOutSame ? !out_over_in(so, sr, M) : !apart(so, sr, M)) return GBN_EINVAL;
+        if (!apart(so, sh, M) || !out_over_in(sh, sx, M) || !out_over_in(sh, sr, M)) return GBN_EINVAL;
+    }
+    DevInfo d;
+    if ((st = device_info(&d)) != GBN_OK) return st;
+    OutParams p{};
+    p.x = x; p.res = has_res ? res : nullptr; p.gamma = gamma; p.h = has_res ? h : nullptr; p.out = out;
+    p.rstd = rstd; p.scale = scale; p.eps = eps; p.M = M; p.N = static_cast<int>(N);
+    p.ld_x = ld_x; p.ld_res = ld_res; p.ld_h = ld_h; p.ld_out = ld_out;
+    return cuda_status(launch_rms_out_plain(dtype, kind, group != 0, p, d.sms, stream));
+}
+
+int out_kind(int q_dtype) { return q_dtype == GBN_E4M3 ? kOutE4M3 : q_dtype == GBN_INT8 ? kOutInt8 : -1; }
+
+int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *gamma, const float *rstd, void *dx,
+                     void *dgamma, int64_t M, int64_t N, int dtype, void *workspace, size_t workspace_bytes_given,
+                     int64_t ld_dh, const gbn_options *opt, cudaStream_t stream) {
+    int st = check_shape(M, N, dtype);
+    Opts o;
+    if (st == GBN_OK) st = resolve_options(opt, N, dtype, &o);
+    if (st != GBN_OK) return st;
+    if (!ld_dh) ld_dh = N;
+    if (ld_dh < N || o.reduce_mode != GBN_REDUCE_PARTIALS || o.kernel == GBN_KERNEL_SLOT || !dgamma) return GBN_EINVAL;
+    if (M > 0) {
+        if (!dy || !dh || !h || !gamma || !rstd || !dx || !workspace) return GBN_EINVAL;
+        const int64_t es = elem_bytes(dtype);
+        const RowSpan sdx{dx, o.ld_out * es, N * es}, sdy{dy, o.ld_dy * es, N * es}, sdh{dh, ld_dh * es, N * es},
+            sh{h, o.ld_x * es, N * es};
+        if (!out_over_in(sdx, sdy, M) || !out_over_in(sdx, sdh, M) || !out_over_in(sdx, sh, M)) return GBN_EINVAL;
+        DevInfo d;
+        if ((st = device_info(&d)) != GBN_OK) return st;
+        if (workspace_bytes_given < workspace_bytes(M, N, false, d)) return GBN_EWORKSPACE;
+        AddBwdParams p{};
+        p.dy = dy; p.dh = dh; p.h = h; p.gamma = gamma; p.rstd = rstd; p.dx = dx;
+        p.part = workspace_partials(workspace);
+        p.M = M; p.N = static_cast<int>(N); p.ldp = partial_ld(N); p.G = grid_rows(M, d);
+        p.ld_dy = o.ld_dy; p.ld_dh = ld_dh; p.ld_h = o.ld_x; p.ld_dx = o.ld_out;
+        st = cuda_status(launch_rms_add_bwd_plain(dtype, p, stream));
+        if (st != GBN_OK) return st;
+    }
+    return reduce_impl(workspace, workspace_bytes_given, M, N, dtype, false, dgamma, nullptr, o, stream);
+}
+
+// descriptors of device tensors: known types, aligned to their elements,
+// few enough chunks for the kernels' 32-bit counts
+bool valid_tensors(const gbn_tensor *t, int64_t count) {
+    if (count < 0 || (count > 0 && !t)) return false;
+    int64_t vecs = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (t[i].n < 0 || t[i].n > (int64_t(1) << 40) || !valid_dtype(t[i].dtype) || t[i].reserved != 0) return false;
+        if (t[i].n == 0) continue;
+        if (!t[i].data || (reinterpret_cast<uintptr_t>(t[i].data) & (elem_bytes(t[i].dtype) - 1))) return false;
+        vecs += t[i].n / 4 / kGradChunkVecs + 1;
+    }
+    return vecs < (int64_t(1) << 31);
+}
+
+double *grad_partials(void *ws) { return reinterpret_cast<double *>(workspace_partials(ws)); }
+
+size_t grad_workspace(const DevInfo &d) { return (size_t)d.sms * kGradCtasPerSm * sizeof(double) + 256; }
+
 }  // namespace
 }  // namespace gbn
 
 using namespace gbn;
 
 extern "C" {
+
+int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y, void *h, float *rstd, float eps,
+                int64_t M, int64_t N, int dtype, int64_t ld_x, int64_t ld_res, int64_t ld_y, int64_t ld_h, int kernel,
+                cudaStream_t stream) {
+    return rms_out_impl(kOutSame, 0, x, residual, true, gamma, y, nullptr, h, rstd, eps, M, N, dtype, ld_x, ld_res,
+                        ld_y, ld_h, kernel, stream);
+}
+
+int rms_fwd_q8(const void *x, const void *gamma, void *q, float *scale, float *rstd, float eps, int64_t M, int64_t N,
+               int dtype, int q_dtype, int64_t group, int64_t ld_x, int64_t ld_q, int kernel, cudaStream_t stream) {
+    const int kind = out_kind(q_dtype);
+    if (kind < 0) return GBN_EDTYPE;
+    return rms_out_impl(kind, group, x, nullptr, false, gamma, q, scale, nullptr, rstd, eps, M, N, dtype, ld_x, 0,
+                        ld_q, 0, kernel, stream);
+}
+
+int rms_add_fwd_q8(const void *x, const void *residual, const void *gamma, void *q, float *scale, void *h, float *rstd,
+                   float eps, int64_t M, int64_t N, int dtype, int q_dtype, int64_t group, int64_t ld_x,
+                   int64_t ld_res, int64_t ld_q, int64_t ld_h, int kernel, cudaStream_t stream) {
+    const int kind = out_kind(q_dtype);
+    if (kind < 0) return GBN_EDTYPE;
+    return rms_out_impl(kind, group, x, residual, true, gamma, q, scale, h, rstd, eps, M, N, dtype, ld_x, ld_res,
+                        ld_q, ld_h, kernel, stream);
+}
+
+int rms_add_bwd(const void *dy, const void *dh, const void *h, const void *gamma, const float *rstd, void *dx,
+                void *dgamma, int64_t M, int64_t N, int dtype, void *workspace, size_t workspace_bytes, int64_t ld_dh,
+                const gbn_options *opt, cudaStream_t stream) {
+    return rms_add_bwd_impl(dy, dh, h, gamma, rstd, dx, dgamma, M, N, dtype, workspace, workspace_bytes, ld_dh, opt,
+                            stream);
+}
+
+size_t gbn_grad_workspace_bytes(void) {
+    DevInfo d;
+    if (device_info(&d) != GBN_OK) return 0;
+    return grad_workspace(d);
+}
+
+int gbn_grad_norm(const gbn_tensor *tensors, int64_t count, float *norm, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream) {
+    if (!valid_tensors(tensors, count) || !norm || !workspace) return GBN_EINVAL;
+    DevInfo d;
+    const int st = device_info(&d);
+    if (st != GBN_OK) return st;
+    if (workspace_bytes < grad_workspace(d)) return GBN_EWORKSPACE;
+    return cuda_status(launch_grad_norm(tensors, count, norm, grad_partials(workspace), d.sms, stream));
+}
+
+int gbn_grad_clip(const gbn_tensor *tensors, const gbn_tensor *out, int64_t count, float max_norm, float eps,
+                  float *norm, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!valid_tensors(tensors, count) || !norm || !workspace) return GBN_EINVAL;
+    if (!(max_norm >= 0.f) || !(eps >= 0.f)) return GBN_EINVAL;
+    if (out) {
+        if (!valid_tensors(out, count)) return GBN_EINVAL;
+        for (int64_t i = 0; i < count; ++i)
+            if (out[i].n != tensors[i].n || out[i].dtype != tensors[i].dtype) return GBN_EINVAL;
+    }
+    DevInfo d;
+    const int st = device_info(&d);
+    if (st != GBN_OK) return st;
+    if (workspace_bytes < grad_workspace(d)) return GBN_EWORKSPACE;
+    return cuda_status(launch_grad_clip(tensors, out, count, max_norm, eps, norm, grad_partials(workspace), d.sms,
+                                        stream));
+}
+
+int gbn_grad_check(const gbn_tensor *tensors, int64_t count) {
+    if (!valid_tensors(tensors, count)) return GBN_EINVAL;
+    try {
+        std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+        spans.reserve(static_cast<size_t>(count));
+        for (int64_t i = 0; i < count; ++i)
+            if (tensors[i].n > 0) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(tensors[i].data);
+                spans.emplace_back(a, a + tensors[i].n * elem_bytes(tensors[i].dtype));
+            }
+        std::sort(spans.begin(), spans.end());
+        for (size_t i = 1; i < spans.size(); ++i)
+            if (spans[i].first < spans[i - 1].second) return GBN_EINVAL;
+    } catch (...) {  // no host memory for the list
+        return GBN_EINVAL;
+    }
+    return GBN_OK;
+}
 
 size_t gbn_bwd_workspace_bytes(int64_t M, int64_t N, int dtype, int has_beta) {
     if (check_shape(M, N, dtype) != GBN_OK || M <= 0) return 0;

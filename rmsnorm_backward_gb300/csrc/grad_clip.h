@@ -1,0 +1,29 @@
+// grad_clip.h -- tables and launch functions of the global gradient norm and
+// the clip (grad_clip.cu).  Internal to libgbnorm.so.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gbnorm.h"
+
+namespace gbn {
+
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;                                 // 16-byte vectors a thread takes of a chunk
+constexpr int kGradChunkVecs = kGradThreads * kGradVecs;     // 16 KiB
+constexpr int kGradCtasPerSm = 6;
+
+// CTAs for `chunks` chunks in all, and the doubles of workspace: one per CTA
+inline int grad_grid(int64_t chunks, int sms) {
+    const int64_t most = static_cast<int64_t>(sms) * kGradCtasPerSm;
+    return static_cast<int>(chunks < 1 ? 1 : chunks < most ? chunks : most);
+}
+
+cudaError_t launch_grad_norm(const gbn_tensor *g, int64_t count, float *norm, double *partial, int sms,
+                             cudaStream_t s);
+cudaError_t launch_grad_clip(const gbn_tensor *g, const gbn_tensor *out, int64_t count, float max_norm, float eps,
+                             float *norm, double *partial, int sms, cudaStream_t s);
+
+}  // namespace gbn

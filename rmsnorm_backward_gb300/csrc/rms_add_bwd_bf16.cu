@@ -1,0 +1,11 @@
+// rms_add_bwd_bf16.cu -- the backward kernels with the residual's gradient for __nv_bfloat16 storage
+// (templates in rms_add_bwd_kernels.cuh).
+#include "rms_add_bwd_kernels.cuh"
+
+namespace gbn {
+
+cudaError_t launch_rms_add_bwd_plain_bf16(const AddBwdParams &p, cudaStream_t s) {
+    return rms_add_bwd_plain_dispatch<__nv_bfloat16>(p, s);
+}
+
+}  // namespace gbn

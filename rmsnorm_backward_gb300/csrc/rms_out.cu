@@ -1,0 +1,19 @@
+// rms_out.cu -- dtype dispatch of the residual / 8-bit RMSNorm forward.
+#include "rms_out.h"
+
+namespace gbn {
+
+cudaError_t launch_rms_out_plain_f32(int, bool, const OutParams &, int, cudaStream_t);
+cudaError_t launch_rms_out_plain_f16(int, bool, const OutParams &, int, cudaStream_t);
+cudaError_t launch_rms_out_plain_bf16(int, bool, const OutParams &, int, cudaStream_t);
+
+cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParams &p, int sms, cudaStream_t s) {
+    switch (dtype) {
+        case 0: return launch_rms_out_plain_f32(kind, group, p, sms, s);
+        case 1: return launch_rms_out_plain_f16(kind, group, p, sms, s);
+        case 2: return launch_rms_out_plain_bf16(kind, group, p, sms, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gbn

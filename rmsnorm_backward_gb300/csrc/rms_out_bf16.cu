@@ -1,0 +1,10 @@
+// rms_out_bf16.cu -- the residual / 8-bit forward kernels for __nv_bfloat16 storage (templates in rms_out_kernels.cuh).
+#include "rms_out_kernels.cuh"
+
+namespace gbn {
+
+cudaError_t launch_rms_out_plain_bf16(int kind, bool group, const OutParams &p, int sms, cudaStream_t s) {
+    return rms_out_plain_dispatch<__nv_bfloat16>(kind, group, p, sms, s);
+}
+
+}  // namespace gbn

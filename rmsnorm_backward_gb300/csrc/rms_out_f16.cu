@@ -1,0 +1,10 @@
+// rms_out_f16.cu -- the residual / 8-bit forward kernels for __half storage (templates in rms_out_kernels.cuh).
+#include "rms_out_kernels.cuh"
+
+namespace gbn {
+
+cudaError_t launch_rms_out_plain_f16(int kind, bool group, const OutParams &p, int sms, cudaStream_t s) {
+    return rms_out_plain_dispatch<__half>(kind, group, p, sms, s);
+}
+
+}  // namespace gbn
