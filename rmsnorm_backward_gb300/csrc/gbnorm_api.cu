@@ -675,6 +675,12 @@ bool apart(const RowSpan &a, const RowSpan &b, int64_t M) {
 // an output against an input row by row: apart, or the same rows (updated in place)
 bool out_over_in(const RowSpan &out, const RowSpan &in, int64_t M) { return same_rows(out, in) || apart(out, in, M); }
 
+// whether every address is a multiple of the element (null ones are told apart elsewhere)
+template <typename... P>
+bool element_aligned(int64_t es, P... q) {
+    return ((reinterpret_cast<uintptr_t>(q) | ...) & (es - 1)) == 0;
+}
+
 bool valid_eps(float eps) { return eps >= 0.f && isfinite(eps); }
 
 // kind: an OutKind; h and res both given or both null
@@ -693,6 +699,8 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     if (M == 0) return GBN_OK;
     if (!x || !gamma || !out || !rstd || (has_res && (!res || !h)) || (kind != kOutSame && !scale)) return GBN_EINVAL;
     const int64_t es = elem_bytes(dtype), eo = kind == kOutSame ? es : 1;
+    if (!element_aligned(es, x, res, gamma, h) || !element_aligned(eo, out) || !element_aligned(4, rstd, scale))
+        return GBN_EINVAL;
     const RowSpan sx{x, ld_x * es, N * es}, sr{res, ld_res * es, N * es}, sh{h, ld_h * es, N * es},
         so{out, ld_out * eo, N * eo};
     if (kind == kOutSame ? !out_over_in(so, sx, M) : !apart(so, sx, M)) return GBN_EINVAL;
@@ -711,6 +719,65 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
 
 int out_kind(int q_dtype) { return q_dtype == GBN_E4M3 ? kOutE4M3 : q_dtype == GBN_INT8 ? kOutInt8 : -1; }
 
+// Launch shape of the ring kernel of rms_add_bwd, if the four tensors' rows
+// lie alike to 16-byte boundaries and two stages of a row fit; fills the
+// kernel's fields of p (and G, which the phases may lower).
+struct AddBwdPlan {
+    bool ok = false, shift = false;
+    int nv = 0;
+    size_t smem = 0;
+};
+
+AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
+    AddBwdPlan P;
+    const int es = elem_bytes(dtype), V = 16 / es;
+    const auto off = [&](const void *q) { return static_cast<int>((reinterpret_cast<uintptr_t>(q) & 15) / es); };
+    const auto step = [&](int64_t ld) { return static_cast<int>(ld & (V - 1)); };
+    const int o = off(p->h), st = step(p->ld_h);
+    if (off(p->dy) != o || off(p->dh) != o || off(p->dx) != o || step(p->ld_dy) != st || step(p->ld_dh) != st ||
+        step(p->ld_dx) != st)
+        return P;
+    p->shift0 = o;
+    p->shift_step = st;
+    p->phases = 1;
+    while ((p->phases * st) & (V - 1)) p->phases *= 2;
+    P.shift = o != 0 || st != 0 || p->N % V != 0;
+    int most = 0;  // the largest shift of a row
+    for (int r = 0; r < p->phases && r < p->M; ++r) {
+        const int s = row_shift(r, o, st, V);
+        most = s > most ? s : most;
+    }
+    p->nvec = (most + p->N + V - 1) / V;
+    int G = p->G;
+    if (p->M >= p->phases && G >= p->phases) G = G / p->phases * p->phases;
+    p->stat_rows = 0;
+    const int per = G >= p->phases ? G / p->phases : 1;
+    p->stat_rows = static_cast<int>(((p->M + p->phases - 1) / p->phases + per - 1) / per);
+    if (G < p->phases && p->M > G) return P;
+    // vectors a thread owns: 16 elements, then 32
+    int W = 0;
+    for (int elems = 16; elems <= 32 && !W; elems *= 2)
+        for (int w = 1; w <= kAddBwdThreads / 32 && !W; w *= 2)
+            if ((int64_t)32 * w * (elems / V) >= p->nvec) W = w;
+    if (!W) return P;
+    p->tpr = 32 * W;
+    int nv = (p->nvec + p->tpr - 1) / p->tpr;
+    while (nv & (nv - 1)) ++nv;
+    const int slots = kAddBwdThreads / p->tpr;
+    for (int S = 16; S >= 2; --S) {
+        const AddBwdLayout L = add_bwd_layout(slots, S, p->nvec, p->stat_rows);
+        if (L.total <= static_cast<size_t>(d.smem_optin)) {
+            p->stages = S;
+            p->G = G;
+            P.ok = true;
+            P.nv = nv;
+            P.smem = L.total;
+            break;
+        }
+    }
+    return P;
+}
+
 int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *gamma, const float *rstd, void *dx,
                      void *dgamma, int64_t M, int64_t N, int dtype, void *workspace, size_t workspace_bytes_given,
                      int64_t ld_dh, const gbn_options *opt, cudaStream_t stream) {
@@ -723,6 +790,9 @@ int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *
     if (M > 0) {
         if (!dy || !dh || !h || !gamma || !rstd || !dx || !workspace) return GBN_EINVAL;
         const int64_t es = elem_bytes(dtype);
+        if (!element_aligned(es, dy, dh, h, gamma, dx) || !element_aligned(4, rstd) ||
+            !element_aligned(elem_bytes(o.grad_dtype), dgamma))
+            return GBN_EINVAL;
         const RowSpan sdx{dx, o.ld_out * es, N * es}, sdy{dy, o.ld_dy * es, N * es}, sdh{dh, ld_dh * es, N * es},
             sh{h, o.ld_x * es, N * es};
         if (!out_over_in(sdx, sdy, M) || !out_over_in(sdx, sdh, M) || !out_over_in(sdx, sh, M)) return GBN_EINVAL;
@@ -734,8 +804,15 @@ int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *
         p.part = workspace_partials(workspace);
         p.M = M; p.N = static_cast<int>(N); p.ldp = partial_ld(N); p.G = grid_rows(M, d);
         p.ld_dy = o.ld_dy; p.ld_dh = ld_dh; p.ld_h = o.ld_x; p.ld_dx = o.ld_out;
-        st = cuda_status(launch_rms_add_bwd_plain(dtype, p, stream));
+        p.err = d.err;
+        p.wait_ns = o.wait_ns;
+        const AddBwdPlan P = o.kernel == GBN_KERNEL_AUTO ? add_bwd_plan(dtype, d, &p) : AddBwdPlan();
+        st = cuda_status(P.ok ? launch_rms_add_bwd_ring(dtype, P.nv, P.shift, p, P.smem, stream)
+                              : launch_rms_add_bwd_plain(dtype, p, stream));
         if (st != GBN_OK) return st;
+        // the partial rows of the CTAs that ran
+        return cuda_status(launch_colsum(p.part, p.G, p.ldp, p.N, dgamma, nullptr, o.grad_dtype, o.accumulate,
+                                         colsum_small(dtype, N, d), d.sms, stream));
     }
     return reduce_impl(workspace, workspace_bytes_given, M, N, dtype, false, dgamma, nullptr, o, stream);
 }

@@ -16,4 +16,18 @@ cudaError_t launch_rms_add_bwd_plain(int dtype, const AddBwdParams &p, cudaStrea
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_rms_add_bwd_ring_f32(int, bool, const AddBwdParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_add_bwd_ring_f16(int, bool, const AddBwdParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_add_bwd_ring_bf16(int, bool, const AddBwdParams &, size_t, cudaStream_t);
+
+cudaError_t launch_rms_add_bwd_ring(int dtype, int nv, bool shift, const AddBwdParams &p, size_t smem,
+                                    cudaStream_t s) {
+    switch (dtype) {
+        case 0: return launch_rms_add_bwd_ring_f32(nv, shift, p, smem, s);
+        case 1: return launch_rms_add_bwd_ring_f16(nv, shift, p, smem, s);
+        case 2: return launch_rms_add_bwd_ring_bf16(nv, shift, p, smem, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace gbn

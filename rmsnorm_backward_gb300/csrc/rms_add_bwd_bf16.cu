@@ -8,4 +8,8 @@ cudaError_t launch_rms_add_bwd_plain_bf16(const AddBwdParams &p, cudaStream_t s)
     return rms_add_bwd_plain_dispatch<__nv_bfloat16>(p, s);
 }
 
+cudaError_t launch_rms_add_bwd_ring_bf16(int nv, bool shift, const AddBwdParams &p, size_t smem, cudaStream_t s) {
+    return rms_add_bwd_ring_dispatch<__nv_bfloat16>(nv, shift, p, smem, s);
+}
+
 }  // namespace gbn

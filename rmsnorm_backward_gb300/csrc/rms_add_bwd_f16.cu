@@ -8,4 +8,8 @@ cudaError_t launch_rms_add_bwd_plain_f16(const AddBwdParams &p, cudaStream_t s) 
     return rms_add_bwd_plain_dispatch<__half>(p, s);
 }
 
+cudaError_t launch_rms_add_bwd_ring_f16(int nv, bool shift, const AddBwdParams &p, size_t smem, cudaStream_t s) {
+    return rms_add_bwd_ring_dispatch<__half>(nv, shift, p, smem, s);
+}
+
 }  // namespace gbn

@@ -8,4 +8,8 @@ cudaError_t launch_rms_add_bwd_plain_f32(const AddBwdParams &p, cudaStream_t s) 
     return rms_add_bwd_plain_dispatch<float>(p, s);
 }
 
+cudaError_t launch_rms_add_bwd_ring_f32(int nv, bool shift, const AddBwdParams &p, size_t smem, cudaStream_t s) {
+    return rms_add_bwd_ring_dispatch<float>(nv, shift, p, smem, s);
+}
+
 }  // namespace gbn

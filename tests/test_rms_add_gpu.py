@@ -142,7 +142,8 @@ def check_backward(t, h, rstd, dx, dgamma, before=None):
 
 
 SHAPES = [(1, 1), (1, 8), (2, 7), (1, 4096), (3, 4097), (5, 256), (4, 127), (7, 1000), (33, 1024), (160, 498),
-          (64, 2052), (70, 8192), (19, 8193), (9, 16384), (305, 640), (2, 40000), (1000, 72), (513, 130)]
+          (64, 2052), (70, 8192), (19, 8193), (9, 16384), (305, 640), (2, 40000), (1000, 72), (513, 130),
+          (1700, 515), (311, 8191), (8, 12), (9, 9), (155, 4100)]
 
 
 @pytest.mark.parametrize("kernel", ["auto", "plain"])
