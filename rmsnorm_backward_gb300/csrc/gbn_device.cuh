@@ -127,6 +127,12 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
                  : "memory");
 }
 
+// raises the transaction count that the current phase waits for
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
+                 : "memory");
+}
+
 // one arrival (release semantics: this thread's earlier writes are visible
 // to a thread that then observes the phase complete)
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {

@@ -750,27 +750,39 @@ AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
     p->nvec = (most + p->N + V - 1) / V;
     int G = p->G;
     if (p->M >= p->phases && G >= p->phases) G = G / p->phases * p->phases;
-    p->stat_rows = 0;
-    const int per = G >= p->phases ? G / p->phases : 1;
-    p->stat_rows = static_cast<int>(((p->M + p->phases - 1) / p->phases + per - 1) / per);
     if (G < p->phases && p->M > G) return P;
-    // vectors a thread owns: 16 elements, then 32
-    int W = 0;
-    for (int elems = 16; elems <= 32 && !W; elems *= 2)
-        for (int w = 1; w <= kAddBwdThreads / 32 && !W; w *= 2)
-            if ((int64_t)32 * w * (elems / V) >= p->nvec) W = w;
-    if (!W) return P;
-    p->tpr = 32 * W;
-    int nv = (p->nvec + p->tpr - 1) / p->tpr;
-    while (nv & (nv - 1)) ++nv;
-    const int slots = kAddBwdThreads / p->tpr;
-    for (int S = 16; S >= 2; --S) {
-        const AddBwdLayout L = add_bwd_layout(slots, S, p->nvec, p->stat_rows);
+    p->stat_rows = static_cast<int>((p->M + G - 1) / G);
+    // Vectors a thread owns: one for rows of a single warp, else the fewest
+    // from two on that keep 14 of the 16 warps busy (4096 columns of bf16: 2
+    // 83.7 us, 3 85.5, 4 92.7; 1400 of float32: 2, with 12 warps, 58.8, 3
+    // 57.5), else the fewest that fit.
+    const int whole = p->N / V;  // vectors wholly in a row, at most
+    const int64_t stage = (int64_t)p->nvec * 48;
+    const int64_t room = static_cast<int64_t>(d.smem_optin) - 1024 - p->stat_rows * 4;
+    int busy = 0;
+    for (int n : {1, 2, 3, 4, 6, 8}) {
+        if (n * V > 32 || (n == 1 && whole > 32) || busy >= 14) continue;
+        int w = (whole + 32 * n - 1) / (32 * n);
+        if (w < 1) w = 1;
+        if (w > kAddBwdThreads / 32) continue;
+        int slots = kAddBwdThreads / 32 / w;
+        const int64_t fit = (room - (add_bwd_gamma_smem(es, n) ? stage / 3 : 0)) / stage / 2;  // two stages each
+        if (slots > fit) slots = static_cast<int>(fit);
+        if (slots < 1 || (busy && slots * w < 14)) continue;
+        busy = slots * w, p->tpr = 32 * w, p->slots = slots, P.nv = n;
+    }
+    if (!busy) return P;
+    // Stages: about 100 KB of copies in flight, 150 KB where one slot has the
+    // CTA to itself.  More is slower: the reads then run ahead of the writes
+    // and HBM turns around between them less well (4 stages a slot against 2:
+    // 16384x4096 bf16 89.4 against 83.7 us, 65536x1024 89.2 against 81.6).
+    const int64_t want = (p->slots == 1 ? 150 : 100) * 1024 / (p->slots * stage);
+    for (int S = want < 2 ? 2 : want > 16 ? 16 : static_cast<int>(want); S >= 2; --S) {
+        const AddBwdLayout L = add_bwd_layout(p->slots, S, p->nvec, p->stat_rows, add_bwd_gamma_smem(es, P.nv));
         if (L.total <= static_cast<size_t>(d.smem_optin)) {
             p->stages = S;
             p->G = G;
             P.ok = true;
-            P.nv = nv;
             P.smem = L.total;
             break;
         }

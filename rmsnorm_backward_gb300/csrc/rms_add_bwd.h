@@ -23,10 +23,11 @@ struct AddBwdParams {
     int64_t ld_dy, ld_dh, ld_h, ld_dx;  // row strides, in elements
     // the ring kernel only
     int tpr;            // threads per row slot (multiple of 32)
+    int slots;          // rows at once (16 warps hold slots * tpr threads at least)
     int stages;         // ring stages per slot
     int stat_rows;      // most rows of a CTA
-    int nvec;           // 16-byte vectors that a row touches at most
-    int phases;         // CTA b takes rows = b mod phases, all of one shift (see RowPhases)
+    int nvec;           // 16-byte vectors that a row touches, at most
+    int phases;         // G is a multiple of it, or M: a CTA's rows have one shift
     int shift0, shift_step;
     int *err;
     uint64_t wait_ns;
@@ -34,34 +35,36 @@ struct AddBwdParams {
 
 // Rows whose starts are not all on 16 bytes.  Row r starts shift(r) elements
 // after a 16-byte boundary, shift(r) = (shift0 + r * shift_step) mod V with
-// V elements to 16 bytes; rows `phases` apart have the same shift.  A CTA
-// takes rows of one phase only, so its threads' columns stay the same from
-// row to row.
+// V elements to 16 bytes; rows `phases` apart have the same shift.  CTA b
+// takes rows b, b + G, ... with G a multiple of `phases`, so its threads'
+// columns stay the same from row to row.
 __host__ __device__ inline int row_shift(int64_t row, int shift0, int shift_step, int V) {
     return static_cast<int>((shift0 + row * shift_step) & (V - 1));
 }
 
 // shared memory of the ring kernel: ring [slots][stages][3 rows of nvec
-// vectors], reused for the combine of the slots' partial sums | mbarriers
-// [slots][stages] | rstd [stat_rows] | reduction scratch [slots][2][16] |
-// abort flags [slots]
+// vectors], reused for the combine of the slots' partial sums | gamma's
+// vectors, where they are kept there | mbarriers [slots][stages] | rstd
+// [stat_rows] | reduction scratch [slots][2][16] | abort flags [slots]
 struct AddBwdLayout {
-    size_t bar, stat, red, flag, total;
+    size_t gam, bar, stat, red, flag, total;
 };
-__host__ __device__ inline AddBwdLayout add_bwd_layout(int slots, int stages, int nvec, int stat_rows) {
+__host__ __device__ inline AddBwdLayout add_bwd_layout(int slots, int stages, int nvec, int stat_rows, bool gamma) {
     AddBwdLayout L;
-    L.bar = (size_t)slots * stages * 3 * nvec * 16;
+    L.gam = (size_t)slots * stages * 3 * nvec * 16;
+    L.bar = L.gam + (gamma ? (size_t)nvec * 16 : 0);
     L.stat = L.bar + (size_t)slots * stages * 8;
     L.red = (L.stat + (size_t)stat_rows * 4 + 15) / 16 * 16;
     L.flag = L.red + (size_t)slots * 2 * 16 * 4;
     L.total = L.flag + (size_t)slots * 4;
     return L;
 }
+__host__ __device__ constexpr bool add_bwd_gamma_smem(size_t es, int nv) { return es == 2 && nv == 4; }
 
 constexpr int kAddBwdThreads = 512;
 
 cudaError_t launch_rms_add_bwd_plain(int dtype, const AddBwdParams &p, cudaStream_t s);
-// nv: vectors a thread owns (1, 2, 4; float32 also 8); shift: some row does
+// nv: vectors a thread owns (1 to 4; float32 also 6 and 8); shift: some row does
 // not start or end on 16 bytes
 cudaError_t launch_rms_add_bwd_ring(int dtype, int nv, bool shift, const AddBwdParams &p, size_t smem, cudaStream_t s);
 

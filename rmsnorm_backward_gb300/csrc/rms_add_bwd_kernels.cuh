@@ -57,133 +57,152 @@ __global__ void __launch_bounds__(kGenericThreads) rms_add_bwd_plain_kernel(cons
 }
 
 // ---------------------------------------------------------------------------
-// One persistent CTA per SM; its 512 threads are slots of tpr threads, and
-// each slot streams its rows of h, dy and dh through a ring of shared-memory
-// stages filled by 1-D bulk copies.  A thread owns NV column vectors, their
-// gamma and their dgamma sums in registers.  Pass 1 forms sum(dyhat*h) from
-// the stage (one exchange within the slot), pass 2 reads the stage again and
-// writes dx with 16-byte streaming stores: shared memory has the bandwidth for
-// the second read, and registers stay free for rows of up to 32 elements a
-// thread.  The exchange of row k shows that the whole slot is done with row
-// k-1, whose stage is then refilled.
+// One persistent CTA per SM; its 16 warps are slots of tpr threads, and each
+// slot streams its rows of h, dy and dh through a ring of shared-memory
+// stages by 1-D bulk copies, which one warp of the slot issues (a lane for
+// each tensor).  A thread owns NV column vectors, their gamma and their
+// dgamma sums in registers.  Pass 1 takes the row from its stage into
+// registers, as raw vectors, and forms sum(dyhat*h); the exchange of that sum
+// within the slot shows that all of the slot is done with the stage, which is
+// refilled at once; pass 2 writes dx with 16-byte streaming stores.  Where
+// the raw row does not fit in registers (float32, more than 16 elements a
+// thread) pass 2 reads the stage again, which is refilled a row later.  (A producer warp for all slots, with mbarriers for
+// the release, measured slower on aligned rows: 97 against 85 us at
+// 16384x4096 bf16, 80 against 21 us at 32768x256.)
 //
 // SHIFT: rows that do not start or end on 16 bytes.  All four tensors' rows
 // have the same shift (the host checks that), so a row is copied with the up
 // to 14 bytes before and after it that share its first and last 16 bytes
-// (never beyond the tensor's first and last element: those two edges are
-// copied element by element), and the elements beside the row count as zero
-// and are never written.
+// (never beyond the tensor's first and last element: those two ends are
+// copied element by element).  Only the vectors that lie wholly in the row
+// are the threads'; the elements before and after them go to the lanes of the
+// slot's last warp, one each.
 // ---------------------------------------------------------------------------
 template <typename T, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(const AddBwdParams p) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     constexpr int E = NV * V;
+    constexpr bool HOLD = NV <= 4;  // the row kept in registers between the passes,
+    constexpr bool HOLDF = sizeof(T) == 2 && NV <= 2;  // h and dy unpacked
+    // gamma: float32 in registers, or vectors of the storage type in
+    // registers, or those in shared memory, as room in registers allows
+    constexpr bool GFLT = sizeof(T) == 4 || NV <= 2;
+    constexpr bool GSMEM = add_bwd_gamma_smem(sizeof(T), NV);
     extern __shared__ __align__(128) unsigned char smem[];
 
-    const int tid = threadIdx.x, tpr = p.tpr, slots = kAddBwdThreads / tpr;
+    const int tid = threadIdx.x, tpr = p.tpr, W = tpr >> 5, slots = p.slots;
     const int slot = tid / tpr, ts = tid - slot * tpr;
-    const int W = tpr >> 5, warp = ts >> 5, lane = tid & 31;
+    const int warp = ts >> 5, lane = tid & 31;
+    const bool issuer = warp == 0;
     const int N = p.N, S = p.stages;
     const uint32_t rowb = static_cast<uint32_t>(p.nvec) * 16;
-    const AddBwdLayout L = add_bwd_layout(slots, S, p.nvec, p.stat_rows);
-    unsigned char *ring = smem + (size_t)slot * S * 3 * rowb;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L.bar) + slot * S;
+    const AddBwdLayout L = add_bwd_layout(slots, S, p.nvec, p.stat_rows, GSMEM);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar);
     float *st_rstd = reinterpret_cast<float *>(smem + L.stat);
-    float *red = reinterpret_cast<float *>(smem + L.red) + slot * 2 * kRedStride;
-    volatile int *flag = reinterpret_cast<int *>(smem + L.flag) + slot;
+    float *reds = reinterpret_cast<float *>(smem + L.red);
+    int *flags = reinterpret_cast<int *>(smem + L.flag);
 
-    // this CTA's rows: first + step*i for i < nrows
-    const int phase = blockIdx.x % p.phases, step = p.phases;
-    int64_t i0;
-    int nrows;
-    block_rows((p.M - phase + step - 1) / step, (p.G - phase + step - 1) / step, blockIdx.x / step, i0, nrows);
-    const int64_t first = phase + i0 * step;
-    const int s = SHIFT ? row_shift(phase, p.shift0, p.shift_step, V) : 0;
+    // this CTA's rows: first + step*i for i < nrows, all of one phase; the
+    // slot's: i = slot + k*slots
+    const int64_t first = blockIdx.x;
+    const int step = p.G;
+    const int nrows = static_cast<int>((p.M - first + step - 1) / step);
+    const int ns = slot < slots && slot < nrows ? (nrows - slot + slots - 1) / slots : 0;
+    // the row starts s elements into its first vector; vectors [vb, ve) lie
+    // wholly in it
+    const int s = SHIFT ? row_shift(first, p.shift0, p.shift_step, V) : 0;
     const int nvec = SHIFT ? (s + N + V - 1) / V : p.nvec;
-    const int ns = slot < nrows ? (nrows - slot + slots - 1) / slots : 0;
+    const int vb = s > 0 ? 1 : 0, ve = (s + N) / V;
+    // the lane's element beside them, as a place in the staged row: s <= ce < s + N, or -1
+    int ce = -1;
+    if (SHIFT && warp == W - 1) {
+        if (lane < V)
+            ce = s > 0 && lane >= s && lane < s + N ? lane : -1;
+        else if (lane < 2 * V && ve >= vb)
+            ce = ve * V + lane - V < s + N ? ve * V + lane - V : -1;
+    }
 
     if (tid == 0) {
-        uint64_t *all = reinterpret_cast<uint64_t *>(smem + L.bar);
-        for (int i = 0; i < slots * S; ++i) mbar_init(&all[i], 1);
+        for (int i = 0; i < slots * S; ++i) mbar_init(&bars[i], 1);
         fence_barrier_init();
     }
-    if (ts == 0) *flag = 0;
+    for (int i = tid; i < slots * 2 * kRedStride; i += kAddBwdThreads) reds[i] = 0.f;
+    if (tid < slots) flags[tid] = 0;
     __syncthreads();
 
-    // producer (thread 0 of the slot)
+    // lane t < 3 of the issuing warp copies tensor t's rows
+    unsigned char *ring = smem + (size_t)slot * S * 3 * rowb;
+    uint64_t *bar = bars + slot * S;
+    const T *base = static_cast<const T *>(lane == 0 ? p.h : lane == 1 ? p.dy : p.dh);
+    const int64_t ld = lane == 0 ? p.ld_h : lane == 1 ? p.ld_dy : p.ld_dh;
+    const T *src = base + (first + (int64_t)slot * step) * ld - s;
     int issued = 0, pst = 0;
-    auto row_of = [&](int k) { return first + (int64_t)(slot + k * slots) * step; };
-    auto edge = [&](unsigned char *dst, const T *row, int v) {  // one vector of a row, element by element
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int c = v * V + e - s;
-            if (c >= 0 && c < N) reinterpret_cast<T *>(dst)[v * V + e] = row[c];
-        }
-    };
     auto issue = [&]() {
-        const int64_t row = row_of(issued);
-        unsigned char *dst = ring + (size_t)pst * 3 * rowb;
-        const T *src[3] = {static_cast<const T *>(p.h) + row * p.ld_h, static_cast<const T *>(p.dy) + row * p.ld_dy,
-                           static_cast<const T *>(p.dh) + row * p.ld_dh};
-        if constexpr (SHIFT) {
-            const T *base[3] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.dh)};
-            const int64_t ld[3] = {p.ld_h, p.ld_dy, p.ld_dh};
-            int v0[3], v1[3];
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int t = 0; t < 3; ++t) {
-                const T *end = base[t] + (p.M - 1) * ld[t] + N;
-                v0[t] = src[t] - s < base[t] ? 1 : 0;
-                v1[t] = src[t] - s + (int64_t)nvec * V > end ? nvec - 1 : nvec;
-                if (v0[t]) edge(dst + t * rowb, src[t], 0);
-                if (v1[t] < nvec && (nvec > 1 || !v0[t])) edge(dst + t * rowb, src[t], nvec - 1);
-                if (v1[t] > v0[t]) bytes += (v1[t] - v0[t]) * 16;
+        const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
+        uint32_t from = 0, to = bytes;
+        unsigned char *dst = ring + ((size_t)pst * 3 + lane) * rowb;
+        const int64_t row = SHIFT ? first + (int64_t)(slot + issued * slots) * step : 0;
+        if (SHIFT && (row == 0 || row == p.M - 1)) {
+            // the tensors' first and last rows: nothing outside them is read
+            if (lane < 3) {
+                if (src < base) from = 16;
+                if (src + (size_t)nvec * V > base + (p.M - 1) * ld + N) to = bytes - 16;
+                T *d = reinterpret_cast<T *>(dst);
+                for (int c = s; c < s + N && c < static_cast<int>(from / sizeof(T)); ++c) d[c] = src[c];
+                for (int c = max(static_cast<int>(to / sizeof(T)), s); c < s + N; ++c) d[c] = src[c];
+                if (to > from) mbar_expect_tx(&bar[pst], to - from);
             }
-            mbar_arrive_expect_tx(&bar[pst], bytes);
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-                if (v1[t] > v0[t])
-                    bulk_load_nohint(dst + t * rowb + v0[t] * 16, src[t] - s + v0[t] * V, (v1[t] - v0[t]) * 16,
-                                     &bar[pst]);
-        } else {
-            mbar_arrive_expect_tx(&bar[pst], 3 * rowb);
-#pragma unroll
-            for (int t = 0; t < 3; ++t) bulk_load_nohint(dst + t * rowb, src[t], rowb, &bar[pst]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[pst]);
+        } else if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[pst], 3 * bytes);
         }
+        if (lane < 3 && to > from) bulk_load_nohint(dst + from, src + from / sizeof(T), to - from, &bar[pst]);
+        src += (int64_t)slots * step * ld;
         if (++pst == S) pst = 0;
         ++issued;
     };
-    if (ts == 0) {
+    if (issuer)
         while (issued < S && issued < ns) issue();
-    }
 
     for (int i = tid; i < nrows; i += kAddBwdThreads) st_rstd[i] = p.rstd[first + (int64_t)i * step];
-    float gam[E], acc[E];
+    const T *gamma = static_cast<const T *>(p.gamma) - s;  // by place in the staged row
+    float gam[GFLT ? E : 1], acc[E];
+    uint4 graw[GFLT || GSMEM ? 1 : NV];
+    unsigned char *gs = smem + L.gam;
+    if constexpr (GSMEM) {
+        for (int c = vb * V + tid; c < ve * V; c += kAddBwdThreads) reinterpret_cast<T *>(gs)[c] = gamma[c];
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = ts + j * tpr;
+        const int v = vb + ts + j * tpr;
+        float g[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int c = v * V + e - s;
-            gam[j * V + e] = c >= 0 && c < N ? Tr::load1(static_cast<const T *>(p.gamma) + c) : 0.f;
+            if constexpr (!GSMEM) g[e] = v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
             acc[j * V + e] = 0.f;
+            if constexpr (GFLT) gam[j * V + e] = g[e];
         }
+        if constexpr (!GFLT && !GSMEM) graw[j] = Tr::pack(g);
     }
+    const float ge = ce >= 0 ? Tr::load1(gamma + ce) : 0.f;
+    float ae = 0.f;
     __syncthreads();
     griddep_launch_dependents();
 
     const float inv_n = 1.0f / static_cast<float>(N);
-    // elements of vector v beside the row count as zero
-    auto mask = [&](float *f, int v) {
-        if constexpr (SHIFT) {
-            if (v == 0 || v == nvec - 1) {
+    float *red = reds + (slot < slots ? slot : 0) * 2 * kRedStride;
+    volatile int *flag = flags + slot;
+    // vector v of gamma, as pairs' source
+    auto gamma_of = [&](int j, int v, float *g) {
+        if constexpr (GFLT) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int c = v * V + e - s;
-                    if (c < 0 || c >= N) f[e] = 0.f;
-                }
-            }
+            for (int e = 0; e < V; ++e) g[e] = gam[j * V + e];
+        } else if constexpr (GSMEM) {
+            Tr::unpack(ld_shared_v4(gs + v * 16), g);
+        } else {
+            Tr::unpack(graw[j], g);
         }
     };
     RingPos pos;
@@ -195,68 +214,87 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
         const float rs = st_rstd[slot + k * slots];
         // pass 1: sum(dyhat * h), one sum per vector
         float sum[1] = {0.f};
+        uint4 hr[HOLD && !HOLDF ? NV : 1], dr[HOLD && !HOLDF ? NV : 1], er[HOLD ? NV : 1];
+        float hx[HOLDF ? E : 1], dyx[HOLDF ? E : 1];
+        float he = 0.f, de = 0.f, ee = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = ts + j * tpr;
-            if (v < nvec) {
-                float hf[V], df[V];
-                Tr::unpack(ld_shared_v4(sh + v * 16), hf);
-                Tr::unpack(ld_shared_v4(sh + rowb + v * 16), df);
-                mask(hf, v);
-                mask(df, v);
-                float2 t = pair_mul(pair_mul(pair_at(df, 0), pair_at(gam + j * V, 0)), pair_at(hf, 0));
+            const int v = vb + ts + j * tpr;
+            if (v < ve) {
+                float hf[V], df[V], g[V];
+                const uint4 h4 = ld_shared_v4(sh + v * 16), d4 = ld_shared_v4(sh + rowb + v * 16);
+                if constexpr (HOLD) er[j] = ld_shared_v4(sh + 2 * rowb + v * 16);
+                if constexpr (HOLD && !HOLDF) {
+                    hr[j] = h4;
+                    dr[j] = d4;
+                }
+                Tr::unpack(h4, hf);
+                Tr::unpack(d4, df);
+                if constexpr (HOLDF) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) hx[j * V + e] = hf[e], dyx[j * V + e] = df[e];
+                }
+                gamma_of(j, v, g);
+                float2 t = pair_mul(pair_mul(pair_at(df, 0), pair_at(g, 0)), pair_at(hf, 0));
 #pragma unroll
                 for (int i = 1; i < V / 2; ++i)
-                    t = pair_fma(pair_mul(pair_at(df, i), pair_at(gam + j * V, i)), pair_at(hf, i), t);
+                    t = pair_fma(pair_mul(pair_at(df, i), pair_at(g, i)), pair_at(hf, i), t);
                 sum[0] += t.x + t.y;
             }
         }
+        if (SHIFT && ce >= 0) {
+            he = Tr::load1(reinterpret_cast<const T *>(sh) + ce);
+            de = Tr::load1(reinterpret_cast<const T *>(sh + rowb) + ce);
+            ee = Tr::load1(reinterpret_cast<const T *>(sh + 2 * rowb) + ce);
+            sum[0] = fmaf(de * ge, he, sum[0]);
+        }
         if (slot_reduce<1>(sum, red + (k & 1) * kRedStride, flag, timed_out, W, warp, lane, 1 + slot, tpr)) break;
-        // the slot is done with the row before this one: refill its stage
-        if (ts == 0 && issued < ns && k > 0) {
+        // the slot is done with this row's stage (the row before's): refill it
+        if (issuer && issued < ns && (HOLD || k > 0)) {
             fence_proxy_async();
             issue();
         }
-        // pass 2: dx = dyhat*rstd + xhat*a + dh, a = -rstd * mean(dyhat*xhat)
-        const float a = -rs * (sum[0] * rs * inv_n);
+        // pass 2, with D = dy*rstd and a = -rstd^2 * mean(dyhat*xhat):
+        // dgamma += D*h, dx = D*gamma + (h*a + dh)
+        const float a = -rs * rs * (sum[0] * rs * inv_n);
         const float2 rs2 = make_float2(rs, rs), a2 = make_float2(a, a);
-        T *dx = static_cast<T *>(p.dx) + row_of(k) * p.ld_dx - s;
+        T *dx = static_cast<T *>(p.dx) + (first + (int64_t)(slot + k * slots) * step) * p.ld_dx - s;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = ts + j * tpr;
-            if (v < nvec) {
-                float hf[V], df[V], o[V];
-                Tr::unpack(ld_shared_v4(sh + v * 16), hf);
-                Tr::unpack(ld_shared_v4(sh + rowb + v * 16), df);
-                Tr::unpack(ld_shared_v4(sh + 2 * rowb + v * 16), o);
-                mask(hf, v);
-                mask(df, v);
+            const int v = vb + ts + j * tpr;
+            if (v < ve) {
+                float hf[V], df[V], g[V], o[V];
+                if constexpr (HOLDF) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) hf[e] = hx[j * V + e], df[e] = dyx[j * V + e];
+                } else {
+                    Tr::unpack(HOLD ? hr[HOLD && !HOLDF ? j : 0] : ld_shared_v4(sh + v * 16), hf);
+                    Tr::unpack(HOLD ? dr[HOLD && !HOLDF ? j : 0] : ld_shared_v4(sh + rowb + v * 16), df);
+                }
+                Tr::unpack(HOLD ? er[HOLD ? j : 0] : ld_shared_v4(sh + 2 * rowb + v * 16), o);
+                gamma_of(j, v, g);
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
                     const int e = j * V + 2 * i;
-                    const float2 d2 = pair_at(df, i), xh = pair_mul(pair_at(hf, i), rs2);
-                    const float2 ag = pair_fma(d2, xh, make_float2(acc[e], acc[e + 1]));
+                    const float2 D = pair_mul(pair_at(df, i), rs2), h2 = pair_at(hf, i);
+                    const float2 ag = pair_fma(D, h2, make_float2(acc[e], acc[e + 1]));
                     acc[e] = ag.x, acc[e + 1] = ag.y;
-                    const float2 o2 = pair_add(pair_fma(pair_mul(d2, make_float2(gam[e], gam[e + 1])), rs2,
-                                                        pair_mul(xh, a2)), pair_at(o, i));
+                    const float2 o2 = pair_fma(D, pair_at(g, i), pair_fma(h2, a2, pair_at(o, i)));
                     o[2 * i] = o2.x, o[2 * i + 1] = o2.y;
                 }
-                if (SHIFT && (v == 0 || v == nvec - 1)) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const int c = v * V + e - s;
-                        if (c >= 0 && c < N) Tr::store1(dx + v * V + e, o[e]);
-                    }
-                } else {
-                    st_global_cs_v4(dx + (size_t)v * V, Tr::pack(o));
-                }
+                st_global_cs_v4(dx + (size_t)v * V, Tr::pack(o));
             }
+        }
+        if (SHIFT && ce >= 0) {
+            const float D = de * rs;
+            ae = fmaf(D, he, ae);
+            Tr::store1(dx + ce, fmaf(D, ge, fmaf(he, a, ee)));
         }
         pos.next(S);
     }
     // after a wait ran out: let the copies this slot still has in flight land
-    // (bounded) before the CTA exits
-    if (ts == 0) {
+    // (bounded) before the CTA goes on
+    if (issuer && lane == 0) {
         for (int kk = k; kk < issued; ++kk) {
             if (!mbar_wait_bounded(&bar[kk % S], (kk / S) & 1, kDrainNs)) {
                 record_error(p.err, kErrDrain);
@@ -268,22 +306,26 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
     // the CTA's partial row: the slots' sums added in slot order in shared memory
     float *part = p.part + (size_t)blockIdx.x * p.ldp;
     __syncthreads();
-    float *comb = reinterpret_cast<float *>(smem);
     const int width = nvec * V;
+    float *comb = reinterpret_cast<float *>(smem) + (size_t)slot * width;
+    if (slot < slots) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int v = ts + j * tpr;
-        if (v < nvec) {
+        for (int j = 0; j < NV; ++j) {
+            const int v = vb + ts + j * tpr;
+            if (v < ve) {
 #pragma unroll
-            for (int e = 0; e < V; e += 4)
-                *reinterpret_cast<float4 *>(comb + (size_t)slot * width + v * V + e) =
-                    make_float4(acc[j * V + e], acc[j * V + e + 1], acc[j * V + e + 2], acc[j * V + e + 3]);
+                for (int e = 0; e < V; e += 4)
+                    *reinterpret_cast<float4 *>(comb + v * V + e) =
+                        make_float4(acc[j * V + e], acc[j * V + e + 1], acc[j * V + e + 2], acc[j * V + e + 3]);
+            }
         }
+        if (SHIFT && ce >= 0) comb[ce] = ae;
     }
     __syncthreads();
+    comb = reinterpret_cast<float *>(smem) + s;
     for (int c = tid; c < N; c += kAddBwdThreads) {
-        float t = comb[c + s];
-        for (int q = 1; q < slots; ++q) t += comb[(size_t)q * width + c + s];
+        float t = comb[c];
+        for (int q = 1; q < slots; ++q) t += comb[(size_t)q * width + c];
         part[c] = t;
     }
 }
@@ -300,12 +342,22 @@ cudaError_t rms_add_bwd_ring_launch(const AddBwdParams &p, size_t smem, cudaStre
 template <typename T>
 cudaError_t rms_add_bwd_ring_dispatch(int nv, bool shift, const AddBwdParams &p, size_t smem, cudaStream_t s) {
     switch (nv) {
-        case 1: return shift ? rms_add_bwd_ring_launch<T, 1, true>(p, smem, s) : rms_add_bwd_ring_launch<T, 1, false>(p, smem, s);
-        case 2: return shift ? rms_add_bwd_ring_launch<T, 2, true>(p, smem, s) : rms_add_bwd_ring_launch<T, 2, false>(p, smem, s);
-        case 4: return shift ? rms_add_bwd_ring_launch<T, 4, true>(p, smem, s) : rms_add_bwd_ring_launch<T, 4, false>(p, smem, s);
+#define GBN_CASE(n) \
+    case n: return shift ? rms_add_bwd_ring_launch<T, n, true>(p, smem, s) : rms_add_bwd_ring_launch<T, n, false>(p, smem, s)
+        GBN_CASE(1);
+        GBN_CASE(2);
+        GBN_CASE(3);
+        GBN_CASE(4);
+#undef GBN_CASE
+        case 6:
         case 8:
-            if constexpr (sizeof(T) == 4)
-                return shift ? rms_add_bwd_ring_launch<T, 8, true>(p, smem, s) : rms_add_bwd_ring_launch<T, 8, false>(p, smem, s);
+            if constexpr (sizeof(T) == 4) {
+                if (nv == 6)
+                    return shift ? rms_add_bwd_ring_launch<T, 6, true>(p, smem, s)
+                                 : rms_add_bwd_ring_launch<T, 6, false>(p, smem, s);
+                return shift ? rms_add_bwd_ring_launch<T, 8, true>(p, smem, s)
+                             : rms_add_bwd_ring_launch<T, 8, false>(p, smem, s);
+            }
     }
     return cudaErrorInvalidValue;
 }
