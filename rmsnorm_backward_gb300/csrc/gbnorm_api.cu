@@ -681,7 +681,123 @@ bool element_aligned(int64_t es, P... q) {
     return ((reinterpret_cast<uintptr_t>(q) | ...) & (es - 1)) == 0;
 }
 
+// How the rows of several tensors lie to 16-byte boundaries, if all alike.
+struct RowPhases {
+    bool ok = false;
+    bool shift = false;  // some row does not start or end on 16 bytes
+    int shift0 = 0, step = 0;
+    int phases = 1;      // rows this far apart lie alike
+    int nvec = 0;        // vectors that a row touches, at most
+};
+struct RowBase {
+    const void *p;
+    int64_t ld;
+};
+
+template <int K>
+RowPhases row_phases(int es, int64_t M, int N, const RowBase (&t)[K]) {
+    RowPhases r;
+    const int V = 16 / es;
+    const auto off = [&](const RowBase &b) { return static_cast<int>((reinterpret_cast<uintptr_t>(b.p) & 15) / es); };
+    const auto step = [&](const RowBase &b) { return static_cast<int>(b.ld & (V - 1)); };
+    for (int i = 1; i < K; ++i)
+        if (off(t[i]) != off(t[0]) || step(t[i]) != step(t[0])) return r;
+    r.ok = true;
+    r.shift0 = off(t[0]);
+    r.step = step(t[0]);
+    while ((r.phases * r.step) & (V - 1)) r.phases *= 2;
+    r.shift = r.shift0 != 0 || r.step != 0 || N % V != 0;
+    int most = 0;
+    for (int i = 0; i < r.phases && i < M; ++i) {
+        const int s = row_shift(i, r.shift0, r.step, V);
+        most = s > most ? s : most;
+    }
+    r.nvec = (most + N + V - 1) / V;
+    return r;
+}
+
+// CTAs for rows of `phases` phases: a multiple of it, or one for each row
+// (0: neither).
+int phase_grid(int64_t M, int phases, const DevInfo &d, int most) {
+    int G = M < most ? static_cast<int>(M) : most;
+    if (G == M) return G;
+    return G / phases * phases;
+}
+
+// Slots of the ring kernels' 16 warps.
+struct SlotPlan {
+    bool ok = false;
+    int nv = 0, tpr = 0, slots = 0, stages = 0;
+};
+
+// whole: vectors wholly in a row, at most; stage: bytes of one; room(nv,
+// slots): shared memory left for the stages.
+template <typename Room>
+SlotPlan slot_plan(int V, int whole, int64_t stage, Room room) {
+    // Vectors a thread owns: one for rows of a single warp, else the fewest
+    // from two on that keep 14 of the 16 warps busy (rms_add_bwd, 4096 columns
+    // of bf16: 2 83.7 us, 3 85.5, 4 92.7; 1400 of float32: 2, with 12 warps,
+    // 58.8, 3 57.5), else the fewest that fit.
+    SlotPlan P;
+    int busy = 0;
+    for (int n : {1, 2, 3, 4, 6, 8}) {
+        if (n * V > 32 || (n == 1 && whole > 32) || busy >= 14) continue;
+        int w = (whole + 32 * n - 1) / (32 * n);
+        if (w < 1) w = 1;
+        if (w > 16) continue;
+        int slots = 16 / w;
+        const int64_t fit = room(n, slots) / stage / 2;  // two stages each
+        if (slots > fit) slots = static_cast<int>(fit);
+        if (slots < 1 || (busy && slots * w < 14)) continue;
+        busy = slots * w, P.tpr = 32 * w, P.slots = slots, P.nv = n;
+    }
+    if (!busy) return P;
+    // Stages: about 100 KB of copies in flight, 150 KB where one slot has the
+    // CTA to itself.  More is slower: the reads then run ahead of the writes
+    // and HBM turns around between them less well (rms_add_bwd, 4 stages a
+    // slot against 2: 16384x4096 bf16 89.4 against 83.7 us, 65536x1024 89.2
+    // against 81.6).
+    const int64_t want = (P.slots == 1 ? 150 : 100) * 1024 / (P.slots * stage);
+    const int64_t fit = room(P.nv, P.slots) / stage / P.slots;
+    const int64_t S = want < 2 ? 2 : want > 16 ? 16 : want;
+    P.stages = static_cast<int>(S < fit ? S : fit);
+    P.ok = true;
+    return P;
+}
+
 bool valid_eps(float eps) { return eps >= 0.f && isfinite(eps); }
+
+// Launch shape of the ring kernel of the residual / 8-bit forward, if the
+// tensors' rows lie alike to 16-byte boundaries and two stages of a row fit;
+// fills the kernel's fields of p.
+struct OutPlan {
+    bool ok = false, shift = false;
+    int nv = 0;
+    size_t smem = 0;
+};
+
+OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
+    OutPlan P;
+    const int es = elem_bytes(dtype), V = 16 / es, streams = p->res ? 2 : 1;
+    const RowBase x{p->x, p->ld_x};
+    const RowBase res = p->res ? RowBase{p->res, p->ld_res} : x, h = p->res ? RowBase{p->h, p->ld_h} : x;
+    const RowBase out = p->kind == kOutSame ? RowBase{p->out, p->ld_out} : x;
+    const RowPhases r = row_phases(es, p->M, p->N, {x, res, h, out});
+    const int G = phase_grid(p->M, r.phases, d, d.sms);
+    if (!r.ok || G < 1) return P;
+    const int groups = r.shift && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
+    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 16 * streams, [&](int, int slots) {
+        return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(out_layout(slots, 16, 0, 0, groups).total);
+    });
+    if (!s.ok) return P;
+    p->G = G;
+    p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec;
+    p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
+    p->codes_aligned = r.shift0 == 0 && r.step == 0 && reinterpret_cast<uintptr_t>(p->out) % V == 0 && p->ld_out % V == 0;
+    P.ok = true, P.shift = r.shift, P.nv = s.nv;
+    P.smem = out_layout(s.slots, s.stages, streams, r.nvec, groups).total;
+    return P;
+}
 
 // kind: an OutKind; h and res both given or both null
 int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool has_res, const void *gamma, void *out,
@@ -714,6 +830,11 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     p.x = x; p.res = has_res ? res : nullptr; p.gamma = gamma; p.h = has_res ? h : nullptr; p.out = out;
     p.rstd = rstd; p.scale = scale; p.eps = eps; p.M = M; p.N = static_cast<int>(N);
     p.ld_x = ld_x; p.ld_res = ld_res; p.ld_h = ld_h; p.ld_out = ld_out;
+    p.kind = kind; p.group = group != 0; p.err = d.err;
+    if (kernel == GBN_KERNEL_AUTO) {
+        const OutPlan P = out_plan(dtype, d, &p);
+        if (P.ok) return cuda_status(launch_rms_out_ring(dtype, P.nv, P.shift, p, P.smem, stream));
+    }
     return cuda_status(launch_rms_out_plain(dtype, kind, group != 0, p, d.sms, stream));
 }
 
@@ -731,62 +852,22 @@ struct AddBwdPlan {
 AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
     AddBwdPlan P;
     const int es = elem_bytes(dtype), V = 16 / es;
-    const auto off = [&](const void *q) { return static_cast<int>((reinterpret_cast<uintptr_t>(q) & 15) / es); };
-    const auto step = [&](int64_t ld) { return static_cast<int>(ld & (V - 1)); };
-    const int o = off(p->h), st = step(p->ld_h);
-    if (off(p->dy) != o || off(p->dh) != o || off(p->dx) != o || step(p->ld_dy) != st || step(p->ld_dh) != st ||
-        step(p->ld_dx) != st)
-        return P;
-    p->shift0 = o;
-    p->shift_step = st;
-    p->phases = 1;
-    while ((p->phases * st) & (V - 1)) p->phases *= 2;
-    P.shift = o != 0 || st != 0 || p->N % V != 0;
-    int most = 0;  // the largest shift of a row
-    for (int r = 0; r < p->phases && r < p->M; ++r) {
-        const int s = row_shift(r, o, st, V);
-        most = s > most ? s : most;
-    }
-    p->nvec = (most + p->N + V - 1) / V;
-    int G = p->G;
-    if (p->M >= p->phases && G >= p->phases) G = G / p->phases * p->phases;
-    if (G < p->phases && p->M > G) return P;
-    p->stat_rows = static_cast<int>((p->M + G - 1) / G);
-    // Vectors a thread owns: one for rows of a single warp, else the fewest
-    // from two on that keep 14 of the 16 warps busy (4096 columns of bf16: 2
-    // 83.7 us, 3 85.5, 4 92.7; 1400 of float32: 2, with 12 warps, 58.8, 3
-    // 57.5), else the fewest that fit.
-    const int whole = p->N / V;  // vectors wholly in a row, at most
-    const int64_t stage = (int64_t)p->nvec * 48;
-    const int64_t room = static_cast<int64_t>(d.smem_optin) - 1024 - p->stat_rows * 4;
-    int busy = 0;
-    for (int n : {1, 2, 3, 4, 6, 8}) {
-        if (n * V > 32 || (n == 1 && whole > 32) || busy >= 14) continue;
-        int w = (whole + 32 * n - 1) / (32 * n);
-        if (w < 1) w = 1;
-        if (w > kAddBwdThreads / 32) continue;
-        int slots = kAddBwdThreads / 32 / w;
-        const int64_t fit = (room - (add_bwd_gamma_smem(es, n) ? stage / 3 : 0)) / stage / 2;  // two stages each
-        if (slots > fit) slots = static_cast<int>(fit);
-        if (slots < 1 || (busy && slots * w < 14)) continue;
-        busy = slots * w, p->tpr = 32 * w, p->slots = slots, P.nv = n;
-    }
-    if (!busy) return P;
-    // Stages: about 100 KB of copies in flight, 150 KB where one slot has the
-    // CTA to itself.  More is slower: the reads then run ahead of the writes
-    // and HBM turns around between them less well (4 stages a slot against 2:
-    // 16384x4096 bf16 89.4 against 83.7 us, 65536x1024 89.2 against 81.6).
-    const int64_t want = (p->slots == 1 ? 150 : 100) * 1024 / (p->slots * stage);
-    for (int S = want < 2 ? 2 : want > 16 ? 16 : static_cast<int>(want); S >= 2; --S) {
-        const AddBwdLayout L = add_bwd_layout(p->slots, S, p->nvec, p->stat_rows, add_bwd_gamma_smem(es, P.nv));
-        if (L.total <= static_cast<size_t>(d.smem_optin)) {
-            p->stages = S;
-            p->G = G;
-            P.ok = true;
-            P.smem = L.total;
-            break;
-        }
-    }
+    const RowPhases r =
+        row_phases(es, p->M, p->N, {{p->h, p->ld_h}, {p->dy, p->ld_dy}, {p->dh, p->ld_dh}, {p->dx, p->ld_dx}});
+    const int G = phase_grid(p->M, r.phases, d, p->G);
+    if (!r.ok || G < 1) return P;
+    const int stat_rows = static_cast<int>((p->M + G - 1) / G);
+    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 48, [&](int nv, int slots) {
+        const AddBwdLayout L = add_bwd_layout(slots, 16, 0, stat_rows, false);
+        return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(L.total) -
+               (add_bwd_gamma_smem(es, nv) ? r.nvec * 16 : 0);
+    });
+    if (!s.ok) return P;
+    p->G = G;
+    p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec, p->stat_rows = stat_rows;
+    p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
+    P.ok = true, P.shift = r.shift, P.nv = s.nv;
+    P.smem = add_bwd_layout(s.slots, s.stages, r.nvec, stat_rows, add_bwd_gamma_smem(es, s.nv)).total;
     return P;
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "row_phase.h"
+
 namespace gbn {
 
 struct AddBwdParams {
@@ -27,20 +29,10 @@ struct AddBwdParams {
     int stages;         // ring stages per slot
     int stat_rows;      // most rows of a CTA
     int nvec;           // 16-byte vectors that a row touches, at most
-    int phases;         // G is a multiple of it, or M: a CTA's rows have one shift
     int shift0, shift_step;
     int *err;
     uint64_t wait_ns;
 };
-
-// Rows whose starts are not all on 16 bytes.  Row r starts shift(r) elements
-// after a 16-byte boundary, shift(r) = (shift0 + r * shift_step) mod V with
-// V elements to 16 bytes; rows `phases` apart have the same shift.  CTA b
-// takes rows b, b + G, ... with G a multiple of `phases`, so its threads'
-// columns stay the same from row to row.
-__host__ __device__ inline int row_shift(int64_t row, int shift0, int shift_step, int V) {
-    return static_cast<int>((shift0 + row * shift_step) & (V - 1));
-}
 
 // shared memory of the ring kernel: ring [slots][stages][3 rows of nvec
 // vectors], reused for the combine of the slots' partial sums | gamma's

@@ -174,13 +174,15 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
     if constexpr (GSMEM) {
         for (int c = vb * V + tid; c < ve * V; c += kAddBwdThreads) reinterpret_cast<T *>(gs)[c] = gamma[c];
     }
+    const bool gvec = (reinterpret_cast<uintptr_t>(gamma) & 15) == 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = vb + ts + j * tpr;
         float g[V];
+        if (!GSMEM && gvec && v < ve) Tr::unpack(ld_global_nc_v4(gamma + v * V), g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            if constexpr (!GSMEM) g[e] = v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
+            if (!GSMEM && !(gvec && v < ve)) g[e] = v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
             acc[j * V + e] = 0.f;
             if constexpr (GFLT) gam[j * V + e] = g[e];
         }

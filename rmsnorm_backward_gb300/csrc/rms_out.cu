@@ -16,4 +16,17 @@ cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParam
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_rms_out_ring_f32(int, bool, const OutParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_out_ring_f16(int, bool, const OutParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_out_ring_bf16(int, bool, const OutParams &, size_t, cudaStream_t);
+
+cudaError_t launch_rms_out_ring(int dtype, int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
+    switch (dtype) {
+        case 0: return launch_rms_out_ring_f32(nv, shift, p, smem, s);
+        case 1: return launch_rms_out_ring_f16(nv, shift, p, smem, s);
+        case 2: return launch_rms_out_ring_bf16(nv, shift, p, smem, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace gbn

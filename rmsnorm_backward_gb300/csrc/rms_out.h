@@ -26,8 +26,40 @@ struct OutParams {
     int64_t M;
     int N;
     int64_t ld_x, ld_res, ld_h, ld_out;  // row strides, in elements
+    // the ring kernel only
+    int kind;            // OutKind
+    int group;           // scales by groups of kQuantGroup columns
+    int G;               // CTAs: CTA b takes rows b, b + G, ...
+    int tpr;             // threads per row slot (multiple of 32)
+    int slots;           // rows at once
+    int stages;          // ring stages per slot
+    int nvec;            // 16-byte vectors that a row touches, at most
+    int shift0, shift_step;  // row_shift's (row_phase.h)
+    int codes_aligned;   // a vector's codes can be stored at once
+    int *err;
 };
 
+// shared memory of the ring kernel: ring [slots][stages][1 or 2 rows of nvec
+// vectors] | mbarriers [slots][stages] | sums and maxima [slots][2][2][16] |
+// group maxima [slots][3][groups] | abort flags [slots]
+struct OutLayout {
+    size_t bar, red, gmax, flag, total;
+};
+__host__ __device__ inline OutLayout out_layout(int slots, int stages, int streams, int nvec, int groups) {
+    OutLayout L;
+    L.bar = (size_t)slots * stages * streams * nvec * 16;
+    L.red = (L.bar + (size_t)slots * stages * 8 + 15) / 16 * 16;
+    L.gmax = L.red + (size_t)slots * 4 * 16 * 4;
+    L.flag = L.gmax + (size_t)slots * 3 * groups * 4;
+    L.total = L.flag + (size_t)slots * 4;
+    return L;
+}
+
+constexpr int kOutThreads = 512;
+
+// nv: vectors a thread owns (1 to 4; float32 also 6 and 8); shift: some row
+// does not start or end on 16 bytes
+cudaError_t launch_rms_out_ring(int dtype, int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s);
 cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParams &p, int sms, cudaStream_t s);
 
 }  // namespace gbn
