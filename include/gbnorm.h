@@ -396,10 +396,10 @@ int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y,
  * written to h).  With v = gamma * h in float32, a = max |v| over the row
  * (group 0) or over each 128 columns (group 128; the last group may be
  * shorter), and Q = 448 (GBN_E4M3) or 127 (GBN_INT8):
- *   code = round(v * (Q/a)),  scale = rstd * a / Q:  code * scale stands
+ *   code = round(v * (Q/a)),  scale = rstd * a * (1/Q):  code * scale stands
  *   for y = gamma * h * rstd.
- * Q/a, its product with v and the scale are float32 operations, rounded to
- * nearest even, and so is the code.  A row (group) of zeros has codes 0 and
+ * Q/a, its product with v, 1/Q and the scale's two products are float32
+ * operations, rounded to nearest even, and so is the code.  A row (group) of zeros has codes 0 and
  * scale 0; where a row holds a NaN or an infinity, scales and e4m3 codes
  * are NaN as y would be (int8 codes of a NaN are 0).
  *   q [M,N] one byte each (out); scale [M] f32 (group 0) or

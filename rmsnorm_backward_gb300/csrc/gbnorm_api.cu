@@ -740,7 +740,9 @@ SlotPlan slot_plan(int V, int whole, int64_t stage, Room room) {
     // 58.8, 3 57.5), else the fewest that fit.
     SlotPlan P;
     int busy = 0;
+    static const char *fnv = getenv("GBN_NV"), *fs = getenv("GBN_S");
     for (int n : {1, 2, 3, 4, 6, 8}) {
+        if (fnv && n < atoi(fnv)) continue;
         if (n * V > 32 || (n == 1 && whole > 32) || busy >= 14) continue;
         int w = (whole + 32 * n - 1) / (32 * n);
         if (w < 1) w = 1;
@@ -759,6 +761,7 @@ SlotPlan slot_plan(int V, int whole, int64_t stage, Room room) {
     // against 81.6).
     const int64_t want = (P.slots == 1 ? 150 : 100) * 1024 / (P.slots * stage);
     const int64_t fit = room(P.nv, P.slots) / stage / P.slots;
+    if (fs) { P.stages = atoi(fs) < fit ? atoi(fs) : fit; P.ok = true; return P; }
     const int64_t S = want < 2 ? 2 : want > 16 ? 16 : want;
     P.stages = static_cast<int>(S < fit ? S : fit);
     P.ok = true;
@@ -784,7 +787,7 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     const RowBase out = p->kind == kOutSame ? RowBase{p->out, p->ld_out} : x;
     const RowPhases r = row_phases(es, p->M, p->N, {x, res, h, out});
     const int G = phase_grid(p->M, r.phases, d, d.sms);
-    if (!r.ok || G < 1) return P;
+    if (!r.ok || G < 1 || p->M / G >= (1 << 30)) return P;
     const int groups = r.shift && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
     const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 16 * streams, [&](int, int slots) {
         return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(out_layout(slots, 16, 0, 0, groups).total);

@@ -5,10 +5,10 @@
 // Per row of N elements, with T the storage type and Q = 448 (e4m3) or 127
 // (int8):
 //   h = round_T(x + residual)          (no residual: h = x)
-//   rstd = 1 / sqrt(sum(h^2) / N + eps)
+//   rstd = 1 / sqrt(sum(h^2) * (1/N) + eps)
 //   y = round_T(gamma * h * rstd), or, with v = gamma * h,
 //   a = max |v| over the row (or over each group of 128 columns),
-//   code = round(v * (Q / a)),  scale = rstd * a / Q.
+//   code = round(v * (Q / a)),  scale = rstd * a * (1/Q).
 // The statistics are those of the stored h, which the backward reads.  rstd
 // cancels out of the codes, so one pass over the row gives everything that
 // they need, and a code depends on its row's v alone: no order of a sum
@@ -17,6 +17,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "gbn_device.cuh"
 #include "gbn_launch.h"
@@ -39,27 +40,25 @@ __device__ __forceinline__ float warp_max_nan(float v) {
     return v;
 }
 
-// What turns v into a code: code = round((v * pre) * mul).  A maximum so
-// small that Q / a would overflow is first brought up by 2^100, exactly; a
-// row (group) of zeros has codes 0 and scale 0.  a = NaN makes every code
-// NaN (int8: 0) and the scale NaN.
-struct QuantFactors {
-    float pre, mul;
-};
+// What turns v into a code: code = round(v * quant_factor(a)).  Where a is so
+// small that Q / a would overflow, v is first brought up by 2^100, exactly
+// (`tiny`; the factor is then that of the raised a).  A row (group) of zeros
+// has codes 0 and scale 0.  a = NaN makes every code NaN (int8: 0) and the
+// scale NaN.
 template <int KIND>
 __device__ __forceinline__ float quant_top() {
     return KIND == kOutE4M3 ? 448.f : 127.f;
 }
+constexpr float kTiny = 0x1p-100f, kRaise = 0x1p100f;
+__device__ __forceinline__ bool quant_tiny(float a) { return a < kTiny; }
 template <int KIND>
-__device__ __forceinline__ QuantFactors quant_factors(float a) {
-    QuantFactors f;
-    f.pre = a < 0x1p-100f ? 0x1p100f : 1.f;
-    f.mul = a == 0.f ? 0.f : quant_top<KIND>() / (a * f.pre);
-    return f;
+__device__ __forceinline__ float quant_factor(float a) {
+    if (a == 0.f) return 0.f;
+    return quant_top<KIND>() / (quant_tiny(a) ? a * kRaise : a);
 }
 template <int KIND>
 __device__ __forceinline__ float quant_scale(float rstd, float a) {
-    return rstd * a / quant_top<KIND>();
+    return rstd * a * (1.f / quant_top<KIND>());
 }
 
 // four float32 values as four 8-bit codes, the first in the lowest byte
@@ -73,6 +72,22 @@ __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
     } else {
         const int i0 = __float2int_rn(a), i1 = __float2int_rn(b), i2 = __float2int_rn(c), i3 = __float2int_rn(d);
         return (i0 & 255) | ((i1 & 255) << 8) | ((i2 & 255) << 16) | (static_cast<uint32_t>(i3) << 24);
+    }
+}
+// quant4 of finite values up to 127.5 in magnitude.  int8: adding 1.5 * 2^23
+// rounds to the nearest integer, ties to even, and leaves it in the sum's low
+// bits: an addition at full rate for a conversion at an eighth of it.
+template <int KIND>
+__device__ __forceinline__ uint32_t quant4_finite(const float *t) {
+    if constexpr (KIND == kOutE4M3) {
+        return quant4<KIND>(t[0], t[1], t[2], t[3]);
+    } else {
+        constexpr float kRound = 12582912.f;
+        const float2 k2 = make_float2(kRound, kRound);
+        const float2 a = pair_add(make_float2(t[0], t[1]), k2), b = pair_add(make_float2(t[2], t[3]), k2);
+        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
     }
 }
 template <int KIND>
@@ -119,7 +134,7 @@ __global__ void __launch_bounds__(kOutPlainThreads) rms_out_plain_kernel(const O
             }
         }
         q = block_sum(q, sm);
-        const float rs = 1.0f / sqrtf(q * inv_n + p.eps);
+        const float rs = __frsqrt_rn(fmaf(q, inv_n, p.eps));
         if constexpr (KIND != kOutSame && !GROUP) {
             a = warp_max_nan(a);
             if (lane == 0) sx[warp] = a;
@@ -130,8 +145,8 @@ __global__ void __launch_bounds__(kOutPlainThreads) rms_out_plain_kernel(const O
             __syncthreads();
         }
         const T *hr = RES ? h : x;
-        QuantFactors qf = {1.f, 0.f};
-        if constexpr (KIND != kOutSame && !GROUP) qf = quant_factors<KIND>(a);
+        float qf = 0.f, raise = 1.f;
+        if constexpr (KIND != kOutSame && !GROUP) qf = quant_factor<KIND>(a), raise = quant_tiny(a) ? kRaise : 1.f;
         for (int c0 = warp * 128; c0 < N; c0 += NW * 128) {
             float v[4], ga = 0.f;
 #pragma unroll
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(kOutPlainThreads) rms_out_plain_kernel(const O
             }
             if constexpr (GROUP) {
                 ga = warp_max_nan(ga);
-                qf = quant_factors<KIND>(ga);
+                qf = quant_factor<KIND>(ga), raise = quant_tiny(ga) ? kRaise : 1.f;
                 if (lane == 0) p.scale[row * groups + c0 / kQuantGroup] = quant_scale<KIND>(rs, ga);
             }
 #pragma unroll
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(kOutPlainThreads) rms_out_plain_kernel(const O
                     if constexpr (KIND == kOutSame)
                         Tr::store1(static_cast<T *>(p.out) + row * p.ld_out + c, v[i]);
                     else
-                        static_cast<uint8_t *>(p.out)[row * p.ld_out + c] = quant1<KIND>((v[i] * qf.pre) * qf.mul);
+                        static_cast<uint8_t *>(p.out)[row * p.ld_out + c] = quant1<KIND>((v[i] * raise) * qf);
                 }
             }
         }
@@ -224,17 +239,6 @@ __device__ __forceinline__ float round_to(float f) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// quant4 and its factors with the code's type at run time
-__device__ __forceinline__ uint32_t quant4_kind(int kind, const float *t) {
-    return kind == kOutE4M3 ? quant4<kOutE4M3>(t[0], t[1], t[2], t[3]) : quant4<kOutInt8>(t[0], t[1], t[2], t[3]);
-}
-__device__ __forceinline__ QuantFactors factors_kind(int kind, float a) {
-    return kind == kOutE4M3 ? quant_factors<kOutE4M3>(a) : quant_factors<kOutInt8>(a);
-}
-__device__ __forceinline__ float scale_kind(int kind, float rs, float a) {
-    return kind == kOutE4M3 ? quant_scale<kOutE4M3>(rs, a) : quant_scale<kOutInt8>(rs, a);
-}
-
 // Stores a warp's codes, V a lane at consecutive places from `at` of lane 0,
 // of which the first `live` lanes' exist.  Where the places do not start on
 // a multiple of V bytes, a lane joins the end of the lane's before it to its
@@ -270,11 +274,12 @@ __device__ __forceinline__ void store_codes(uint8_t *at, uint2 code, int lane, i
     }
 }
 
-template <typename T, bool QUANT, int NV, bool SHIFT>
+template <typename T, int KIND, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutParams p) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     constexpr int E = NV * V;
+    constexpr bool QUANT = KIND != kOutSame;
     extern __shared__ __align__(128) unsigned char smem[];
 
     const int tid = threadIdx.x, tpr = p.tpr, W = tpr >> 5, slots = p.slots;
@@ -296,8 +301,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     // slot's: i = slot + k*slots
     const int64_t first = blockIdx.x;
     const int step = p.G;
-    const int64_t nrows = (p.M - first + step - 1) / step;
-    const int64_t ns = slot < slots && slot < nrows ? (nrows - slot + slots - 1) / slots : 0;
+    const int nrows = static_cast<int>((p.M - first + step - 1) / step);
+    const int ns = slot < slots && slot < nrows ? (nrows - slot + slots - 1) / slots : 0;
     // the row starts s elements into its first vector; vectors [vb, ve) lie
     // wholly in it
     const int s = SHIFT ? row_shift(first, p.shift0, p.shift_step, V) : 0;
@@ -328,13 +333,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const T *base = static_cast<const T *>(lane == 0 || !res ? p.x : p.res);
     const int64_t ld = lane == 0 || !res ? p.ld_x : p.ld_res;
     const T *src = base + (first + (int64_t)slot * step) * ld - s;
-    int64_t issued = 0;
-    int pst = 0;
+    int issued = 0, pst = 0;
+    const int64_t row_step = (int64_t)slots * step;
+    const int64_t src_step = row_step * ld;
     auto issue = [&]() {
         const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
         uint32_t from = 0, to = bytes;
         unsigned char *dst = ring + ((size_t)pst * streams + lane) * rowb;
-        const int64_t row = SHIFT ? first + (slot + issued * slots) * step : 0;
+        const int64_t row = SHIFT ? first + slot * (int64_t)step + issued * row_step : 0;
         if (SHIFT && (row == 0 || row == p.M - 1)) {
             // the tensors' first and last rows: nothing outside them is read
             if (lane < streams) {
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             mbar_arrive_expect_tx(&bar[pst], streams * bytes);
         }
         if (lane < streams && to > from) bulk_load_nohint(dst + from, src + from / sizeof(T), to - from, &bar[pst]);
-        src += (int64_t)slots * step * ld;
+        src += src_step;
         if (++pst == S) pst = 0;
         ++issued;
     };
@@ -379,16 +385,19 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     volatile int *flag = flags + slot;
     RingPos pos;
     int buf = 0;  // k mod 3
-    int64_t k = 0;
-    for (; k < ns; ++k) {
-        const int64_t row = first + (slot + k * slots) * step;
+    int k = 0;
+    int64_t row = first + slot * (int64_t)step;
+    T *h = static_cast<T *>(p.h) + (res ? row * p.ld_h - s : 0);
+    using Out = typename std::conditional<QUANT, uint8_t, T>::type;
+    Out *out = static_cast<Out *>(p.out) + row * p.ld_out - s;
+    const int64_t h_step = row_step * p.ld_h, out_step = row_step * p.ld_out;
+    for (; k < ns; ++k, row += row_step, h += h_step, out += out_step) {
         const bool timed_out = !mbar_wait_bounded(&bar[pos.stage], pos.parity);
         if (timed_out) record_error(p.err, kErrWaitFull);
         const unsigned char *sx = ring + (size_t)pos.stage * streams * rowb;
         uint32_t *gm = gmax + buf * groups;
         float sum = 0.f, held[E], he = 0.f;
         uint32_t most = 0, vmost[QUANT ? NV : 1];  // |v| as bits: the order of the values, NaN above all
-        T *h = static_cast<T *>(p.h) + row * p.ld_h - s;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = vb + ts + j * tpr;
@@ -493,9 +502,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             fence_proxy_async();
             issue();
         }
-        const float rs = 1.0f / sqrtf(sum * inv_n + p.eps);
+        float rs = 0.f;
+        if (!QUANT || group || ts == 0) rs = __frsqrt_rn(fmaf(sum, inv_n, p.eps));
         if constexpr (!QUANT) {
-            T *y = static_cast<T *>(p.out) + row * p.ld_out - s;
+            T *y = out;
             const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -513,58 +523,73 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             if (SHIFT && ce >= 0) Tr::store1(y + ce, ge * (he * rs));
             if (ts == 0) p.rstd[row] = rs;
         } else {
-            uint8_t *q = static_cast<uint8_t *>(p.out) + row * p.ld_out - s;
+            uint8_t *q = out;
             float *scale = p.scale + (group ? row * groups : row);
-            QuantFactors qf = factors_kind(p.kind, __uint_as_float(most));
-            if (SHIFT && group && ts < groups) {
+            float qf = quant_factor<KIND>(__uint_as_float(most));
+            if (SHIFT && group) {
                 // the maxima of row k-1, read by nobody any more, for row k+2
                 uint32_t *clear = gmax + (buf == 0 ? 2 : buf - 1) * groups;
                 for (int i = ts; i < groups; i += tpr) {
                     clear[i] = 0;
-                    scale[i] = scale_kind(p.kind, rs, __uint_as_float(gm[i]));
+                    scale[i] = quant_scale<KIND>(rs, __uint_as_float(gm[i]));
                 }
             }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int v0 = vb + (ts - lane) + j * tpr, v = v0 + lane;
                 if (v0 >= ve) break;  // the whole warp
-                float t[V];
+                float *t = held + j * V;
+                uint2 code = make_uint2(0, 0);
+                uint32_t m = most;
                 if (SHIFT && group) {
+                    // the vector's columns in one group or two
                     const int c0 = v < ve ? v * V - s : 0, split = kQuantGroup - (c0 & (kQuantGroup - 1));
-                    const QuantFactors f0 = factors_kind(p.kind, __uint_as_float(gm[c0 / kQuantGroup]));
-                    QuantFactors f1 = f0;
-                    if (split < V) f1 = factors_kind(p.kind, __uint_as_float(gm[c0 / kQuantGroup + 1]));
+                    const uint32_t m0 = gm[c0 / kQuantGroup], m1 = split < V ? gm[c0 / kQuantGroup + 1] : m0;
+                    const float f0 = quant_factor<KIND>(__uint_as_float(m0));
+                    const float f1 = split < V ? quant_factor<KIND>(__uint_as_float(m1)) : f0;
+                    const float r0 = quant_tiny(__uint_as_float(m0)) ? kRaise : 1.f;
+                    const float r1 = quant_tiny(__uint_as_float(m1)) ? kRaise : 1.f;
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        t[e] = v < ve ? (held[j * V + e] * (e < split ? f0.pre : f1.pre)) * (e < split ? f0.mul : f1.mul)
-                                      : 0.f;
+                    for (int e = 0; e < V; ++e) t[e] = (t[e] * (e < split ? r0 : r1)) * (e < split ? f0 : f1);
+                    m = max(m0, m1);
                 } else {
                     if (group) {
                         // 128 columns: 16 lanes of a 16-bit type, 32 of float32
-                        uint32_t m = vmost[j];
+                        m = vmost[j];
 #pragma unroll
                         for (int o = kQuantGroup / V / 2; o > 0; o >>= 1)
                             m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        qf = factors_kind(p.kind, __uint_as_float(m));
+                        qf = quant_factor<KIND>(__uint_as_float(m));
                         if ((lane & (kQuantGroup / V - 1)) == 0 && v < ve)
-                            scale[v * V / kQuantGroup] = scale_kind(p.kind, rs, __uint_as_float(m));
+                            scale[v * V / kQuantGroup] = quant_scale<KIND>(rs, __uint_as_float(m));
                     }
+                    if (quant_tiny(__uint_as_float(m))) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] = v < ve ? (held[j * V + e] * qf.pre) * qf.mul : 0.f;
+                        for (int e = 0; e < V; ++e) t[e] *= kRaise;
+                    }
+                    const float2 f2 = make_float2(qf, qf);
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 w = pair_mul(pair_at(t, i), f2);
+                        t[2 * i] = w.x, t[2 * i + 1] = w.y;
+                    }
                 }
-                uint2 code;
-                code.x = quant4_kind(p.kind, t);
-                code.y = V == 8 ? quant4_kind(p.kind, t + (V == 8 ? 4 : 0)) : 0;
+                if (KIND == kOutInt8 && m >= 0x7f800000u) {
+                    code.x = quant4<KIND>(t[0], t[1], t[2], t[3]);
+                    if constexpr (V == 8) code.y = quant4<KIND>(t[4], t[5], t[6], t[7]);
+                } else {
+                    code.x = quant4_finite<KIND>(t);
+                    if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
+                }
                 store_codes<V>(q + (size_t)v0 * V, code, lane, ve - v0 < 32 ? ve - v0 : 32, p.codes_aligned);
             }
             if (SHIFT && ce >= 0) {
-                if (group) qf = factors_kind(p.kind, __uint_as_float(gm[(ce - s) / kQuantGroup]));
-                const float t[4] = {(he * qf.pre) * qf.mul, 0.f, 0.f, 0.f};
-                q[ce] = static_cast<uint8_t>(quant4_kind(p.kind, t));
+                const float a = __uint_as_float(group ? gm[(ce - s) / kQuantGroup] : most);
+                q[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
             }
             if (ts == 0) {
                 p.rstd[row] = rs;
-                if (!group) *scale = scale_kind(p.kind, rs, __uint_as_float(most));
+                if (!group) *scale = quant_scale<KIND>(rs, __uint_as_float(most));
             }
         }
         buf = buf == 2 ? 0 : buf + 1;
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     // after a wait ran out: let the copies this slot still has in flight land
     // (bounded) before the CTA exits
     if (issuer && lane == 0) {
-        for (int64_t kk = k; kk < issued; ++kk) {
+        for (int kk = k; kk < issued; ++kk) {
             if (!mbar_wait_bounded(&bar[kk % S], (kk / S) & 1, kDrainNs)) {
                 record_error(p.err, kErrDrain);
                 break;
@@ -582,20 +607,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     }
 }
 
-template <typename T, bool QUANT, int NV, bool SHIFT>
+template <typename T, int KIND, int NV, bool SHIFT>
 cudaError_t rms_out_ring_launch(const OutParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, QUANT, NV, SHIFT>, done);
+    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, NV, SHIFT>, done);
     if (e != cudaSuccess) return e;
-    rms_out_ring_kernel<T, QUANT, NV, SHIFT><<<p.G, kOutThreads, smem, s>>>(p);
+    rms_out_ring_kernel<T, KIND, NV, SHIFT><<<p.G, kOutThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, bool QUANT>
+template <typename T, int KIND>
 cudaError_t rms_out_ring_nv(int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (nv) {
 #define GBN_CASE(n) \
-    case n: return shift ? rms_out_ring_launch<T, QUANT, n, true>(p, smem, s) : rms_out_ring_launch<T, QUANT, n, false>(p, smem, s)
+    case n: return shift ? rms_out_ring_launch<T, KIND, n, true>(p, smem, s) : rms_out_ring_launch<T, KIND, n, false>(p, smem, s)
         GBN_CASE(1);
         GBN_CASE(2);
         GBN_CASE(3);
@@ -605,10 +630,10 @@ cudaError_t rms_out_ring_nv(int nv, bool shift, const OutParams &p, size_t smem,
         case 8:
             if constexpr (sizeof(T) == 4) {
                 if (nv == 6)
-                    return shift ? rms_out_ring_launch<T, QUANT, 6, true>(p, smem, s)
-                                 : rms_out_ring_launch<T, QUANT, 6, false>(p, smem, s);
-                return shift ? rms_out_ring_launch<T, QUANT, 8, true>(p, smem, s)
-                             : rms_out_ring_launch<T, QUANT, 8, false>(p, smem, s);
+                    return shift ? rms_out_ring_launch<T, KIND, 6, true>(p, smem, s)
+                                 : rms_out_ring_launch<T, KIND, 6, false>(p, smem, s);
+                return shift ? rms_out_ring_launch<T, KIND, 8, true>(p, smem, s)
+                             : rms_out_ring_launch<T, KIND, 8, false>(p, smem, s);
             }
     }
     return cudaErrorInvalidValue;
@@ -616,8 +641,12 @@ cudaError_t rms_out_ring_nv(int nv, bool shift, const OutParams &p, size_t smem,
 
 template <typename T>
 cudaError_t rms_out_ring_dispatch(int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
-    return p.kind == kOutSame ? rms_out_ring_nv<T, false>(nv, shift, p, smem, s)
-                              : rms_out_ring_nv<T, true>(nv, shift, p, smem, s);
+    switch (p.kind) {
+        case kOutSame: return rms_out_ring_nv<T, kOutSame>(nv, shift, p, smem, s);
+        case kOutE4M3: return rms_out_ring_nv<T, kOutE4M3>(nv, shift, p, smem, s);
+        case kOutInt8: return rms_out_ring_nv<T, kOutInt8>(nv, shift, p, smem, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace gbn
