@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -733,16 +734,15 @@ struct SlotPlan {
 // whole: vectors wholly in a row, at most; stage: bytes of one; room(nv,
 // slots): shared memory left for the stages.
 template <typename Room>
-SlotPlan slot_plan(int V, int whole, int64_t stage, Room room) {
+SlotPlan slot_plan(int V, int whole, int64_t stage, int kb, int kb_alone, std::initializer_list<int> counts,
+                   Room room) {
     // Vectors a thread owns: one for rows of a single warp, else the fewest
     // from two on that keep 14 of the 16 warps busy (rms_add_bwd, 4096 columns
     // of bf16: 2 83.7 us, 3 85.5, 4 92.7; 1400 of float32: 2, with 12 warps,
     // 58.8, 3 57.5), else the fewest that fit.
     SlotPlan P;
     int busy = 0;
-    static const char *fnv = getenv("GBN_NV"), *fs = getenv("GBN_S");
-    for (int n : {1, 2, 3, 4, 6, 8}) {
-        if (fnv && n < atoi(fnv)) continue;
+    for (int n : counts) {
         if (n * V > 32 || (n == 1 && whole > 32) || busy >= 14) continue;
         int w = (whole + 32 * n - 1) / (32 * n);
         if (w < 1) w = 1;
@@ -754,14 +754,15 @@ SlotPlan slot_plan(int V, int whole, int64_t stage, Room room) {
         busy = slots * w, P.tpr = 32 * w, P.slots = slots, P.nv = n;
     }
     if (!busy) return P;
-    // Stages: about 100 KB of copies in flight, 150 KB where one slot has the
+    // Stages: about kb KB of copies in flight, kb_alone where one slot has the
     // CTA to itself.  More is slower: the reads then run ahead of the writes
     // and HBM turns around between them less well (rms_add_bwd, 4 stages a
     // slot against 2: 16384x4096 bf16 89.4 against 83.7 us, 65536x1024 89.2
-    // against 81.6).
-    const int64_t want = (P.slots == 1 ? 150 : 100) * 1024 / (P.slots * stage);
+    // against 81.6; rms_add_fwd, 3 against 2: 94.5 against 83.0 at
+    // 16384x4096), the more so the more is written: the 8-bit outputs take
+    // more (16384x4096 of float32 without residual, 2: 56.6, 3: 52.9).
+    const int64_t want = (int64_t)(P.slots == 1 ? kb_alone : kb) * 1024 / (P.slots * stage);
     const int64_t fit = room(P.nv, P.slots) / stage / P.slots;
-    if (fs) { P.stages = atoi(fs) < fit ? atoi(fs) : fit; P.ok = true; return P; }
     const int64_t S = want < 2 ? 2 : want > 16 ? 16 : want;
     P.stages = static_cast<int>(S < fit ? S : fit);
     P.ok = true;
@@ -774,7 +775,7 @@ bool valid_eps(float eps) { return eps >= 0.f && isfinite(eps); }
 // tensors' rows lie alike to 16-byte boundaries and two stages of a row fit;
 // fills the kernel's fields of p.
 struct OutPlan {
-    bool ok = false, shift = false;
+    bool ok = false, full = false;
     int nv = 0;
     size_t smem = 0;
 };
@@ -789,7 +790,12 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     const int G = phase_grid(p->M, r.phases, d, d.sms);
     if (!r.ok || G < 1 || p->M / G >= (1 << 30)) return P;
     const int groups = r.shift && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
-    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 16 * streams, [&](int, int slots) {
+    // without a residual to read, the row's work next to its bytes is more, and
+    // more vectors a thread spread what a row costs besides them (e4m3,
+    // 16384x4096 bf16: 2 52 us, 4 40 us)
+    const std::initializer_list<int> two = {1, 2, 3, 4, 6, 8}, four = {1, 4, 2, 3, 6, 8};
+    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 16 * streams, p->res ? 64 : 96,
+                                 p->kind == kOutSame ? 64 : 128, p->res ? two : four, [&](int, int slots) {
         return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(out_layout(slots, 16, 0, 0, groups).total);
     });
     if (!s.ok) return P;
@@ -797,7 +803,18 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec;
     p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
     p->codes_aligned = r.shift0 == 0 && r.step == 0 && reinterpret_cast<uintptr_t>(p->out) % V == 0 && p->ld_out % V == 0;
-    P.ok = true, P.shift = r.shift, P.nv = s.nv;
+    p->across = r.shift;
+    // wide rows: two stages already are more in flight than HBM likes beside
+    // the writes, so a stage is refilled after its row's stores (8192x16384
+    // bf16 to e4m3 by 128 columns: 157.6 us before them, 142.9 after; on
+    // narrower rows it costs 5%)
+    p->late = p->kind != kOutSame && s.slots == 1 && r.nvec * 16 * streams > 60 * 1024;
+    // neighbouring rows to a CTA's slots, where every CTA has a few rounds of
+    // them; otherwise rows G apart, which all have one shift
+    const bool near = !r.shift && p->M >= (int64_t)4 * G * s.slots;
+    p->cta_step = near ? s.slots : 1;
+    p->slot_step = near ? 1 : G;
+    P.ok = true, P.full = !r.shift && r.nvec == s.nv * s.tpr && s.nv != 3 && s.nv != 6 && (p->kind == kOutSame || p->codes_aligned), P.nv = s.nv;
     P.smem = out_layout(s.slots, s.stages, streams, r.nvec, groups).total;
     return P;
 }
@@ -836,7 +853,7 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     p.kind = kind; p.group = group != 0; p.err = d.err;
     if (kernel == GBN_KERNEL_AUTO) {
         const OutPlan P = out_plan(dtype, d, &p);
-        if (P.ok) return cuda_status(launch_rms_out_ring(dtype, P.nv, P.shift, p, P.smem, stream));
+        if (P.ok) return cuda_status(launch_rms_out_ring(dtype, P.nv, P.full, p, P.smem, stream));
     }
     return cuda_status(launch_rms_out_plain(dtype, kind, group != 0, p, d.sms, stream));
 }
@@ -860,7 +877,7 @@ AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
     const int G = phase_grid(p->M, r.phases, d, p->G);
     if (!r.ok || G < 1) return P;
     const int stat_rows = static_cast<int>((p->M + G - 1) / G);
-    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 48, [&](int nv, int slots) {
+    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 48, 100, 150, {1, 2, 3, 4, 6, 8}, [&](int nv, int slots) {
         const AddBwdLayout L = add_bwd_layout(slots, 16, 0, stat_rows, false);
         return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(L.total) -
                (add_bwd_gamma_smem(es, nv) ? r.nvec * 16 : 0);

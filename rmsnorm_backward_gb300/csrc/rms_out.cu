@@ -20,11 +20,11 @@ cudaError_t launch_rms_out_ring_f32(int, bool, const OutParams &, size_t, cudaSt
 cudaError_t launch_rms_out_ring_f16(int, bool, const OutParams &, size_t, cudaStream_t);
 cudaError_t launch_rms_out_ring_bf16(int, bool, const OutParams &, size_t, cudaStream_t);
 
-cudaError_t launch_rms_out_ring(int dtype, int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
+cudaError_t launch_rms_out_ring(int dtype, int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (dtype) {
-        case 0: return launch_rms_out_ring_f32(nv, shift, p, smem, s);
-        case 1: return launch_rms_out_ring_f16(nv, shift, p, smem, s);
-        case 2: return launch_rms_out_ring_bf16(nv, shift, p, smem, s);
+        case 0: return launch_rms_out_ring_f32(nv, full, p, smem, s);
+        case 1: return launch_rms_out_ring_f16(nv, full, p, smem, s);
+        case 2: return launch_rms_out_ring_bf16(nv, full, p, smem, s);
     }
     return cudaErrorInvalidValue;
 }

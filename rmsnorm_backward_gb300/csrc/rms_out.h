@@ -29,12 +29,15 @@ struct OutParams {
     // the ring kernel only
     int kind;            // OutKind
     int group;           // scales by groups of kQuantGroup columns
-    int G;               // CTAs: CTA b takes rows b, b + G, ...
+    int G;               // CTAs
+    int cta_step, slot_step;  // slot q of CTA b takes rows b*cta_step + q*slot_step + k*G*slots
     int tpr;             // threads per row slot (multiple of 32)
     int slots;           // rows at once
     int stages;          // ring stages per slot
     int nvec;            // 16-byte vectors that a row touches, at most
     int shift0, shift_step;  // row_shift's (row_phase.h)
+    int late;            // a stage is refilled after its row's stores, not before
+    int across;          // some row does not start or end on 16 bytes
     int codes_aligned;   // a vector's codes can be stored at once
     int *err;
 };
@@ -57,9 +60,9 @@ __host__ __device__ inline OutLayout out_layout(int slots, int stages, int strea
 
 constexpr int kOutThreads = 512;
 
-// nv: vectors a thread owns (1 to 4; float32 also 6 and 8); shift: some row
-// does not start or end on 16 bytes
-cudaError_t launch_rms_out_ring(int dtype, int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s);
+// nv: vectors a thread owns (1, 2, 4; float32 also 8); full: every row is
+// nv * tpr whole vectors
+cudaError_t launch_rms_out_ring(int dtype, int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s);
 cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParams &p, int sms, cudaStream_t s);
 
 }  // namespace gbn

@@ -7,8 +7,8 @@ cudaError_t launch_rms_out_plain_bf16(int kind, bool group, const OutParams &p, 
     return rms_out_plain_dispatch<__nv_bfloat16>(kind, group, p, sms, s);
 }
 
-cudaError_t launch_rms_out_ring_bf16(int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
-    return rms_out_ring_dispatch<__nv_bfloat16>(nv, shift, p, smem, s);
+cudaError_t launch_rms_out_ring_bf16(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
+    return rms_out_ring_dispatch<__nv_bfloat16>(nv, full, p, smem, s);
 }
 
 }  // namespace gbn

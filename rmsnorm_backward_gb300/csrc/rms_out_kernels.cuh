@@ -219,12 +219,15 @@ cudaError_t rms_out_plain_dispatch(int kind, bool group, const OutParams &p, int
 // refilled; then the outputs are written from registers: x and residual are
 // read once, h is written once and read by nobody.
 //
-// SHIFT: rows that do not start or end on 16 bytes, all tensors' alike (the
-// host checks that): a row is copied with the up to 14 bytes before and after
-// it that share its first and last 16 bytes (never beyond the tensor's first
-// and last element: those two ends are copied element by element).  Only the
-// vectors that lie wholly in the row are the threads'; the elements before
-// and after them go to the lanes of the slot's last warp, one each.
+// FULL: rows that start and end on 16 bytes (their codes on V) and are as many
+// vectors as the slot's threads own.  Otherwise a thread may own fewer, and rows may lie
+// across 16-byte boundaries, all tensors' alike (the host checks that): such a
+// row is copied with the up to 14 bytes before and after it that share its
+// first and last 16 bytes (never beyond the tensor's first and last element:
+// those two ends are copied element by element); only the vectors that lie
+// wholly in the row are the threads', and the elements before and after them
+// go to the lanes of the slot's last warp, one each.  The maxima of groups
+// then meet in shared memory, as their borders run through vectors.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ float round_to(float f) {
@@ -240,9 +243,10 @@ __device__ __forceinline__ float round_to(float f) {
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
 // Stores a warp's codes, V a lane at consecutive places from `at` of lane 0,
-// of which the first `live` lanes' exist.  Where the places do not start on
-// a multiple of V bytes, a lane joins the end of the lane's before it to its
-// own, and the warp's first and last bytes go one by one.
+// of which the first `live` lanes' exist (live > 0).  Where the places do not
+// start on a multiple of V bytes, a lane joins the end of the lane's before
+// it to its own; the warp's first and last bytes, which have no such
+// neighbour, go one to a lane.
 template <int V>
 __device__ __forceinline__ void store_codes(uint8_t *at, uint2 code, int lane, int live, bool aligned) {
     uint8_t *p = at + lane * V;
@@ -255,62 +259,61 @@ __device__ __forceinline__ void store_codes(uint8_t *at, uint2 code, int lane, i
         }
         return;
     }
-    const unsigned m = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at) & (V - 1));
+    const int m = static_cast<int>(reinterpret_cast<uintptr_t>(at) & (V - 1));
     uint64_t own = code.x;
     if constexpr (V == 8) own |= static_cast<uint64_t>(code.y) << 32;
     const uint64_t prev = __shfl_up_sync(0xffffffffu, own, 1);
-    if (lane < live) {
-        if (lane > 0) {
-            const uint64_t w = m ? (own << (8 * m)) | (prev >> (8 * (V - m))) : own;
-            if constexpr (V == 8)
-                *reinterpret_cast<uint64_t *>(p - m) = w;
-            else
-                *reinterpret_cast<uint32_t *>(p - m) = static_cast<uint32_t>(w);
-        } else {
-            for (unsigned e = 0; e < V - m; ++e) p[e] = static_cast<uint8_t>(own >> (8 * e));
-        }
-        if (lane == live - 1)
-            for (unsigned e = V - m; e < V; ++e) p[e] = static_cast<uint8_t>(own >> (8 * e));
+    if (lane > 0 && lane < live) {
+        const uint64_t w = m ? (own << (8 * m)) | (prev >> (8 * (V - m))) : own;
+        if constexpr (V == 8)
+            *reinterpret_cast<uint64_t *>(p - m) = w;
+        else
+            *reinterpret_cast<uint32_t *>(p - m) = static_cast<uint32_t>(w);
     }
+    // lanes 0 .. V-1: the first lane's bytes below V - m; lanes V .. 2V-1: the
+    // last one's from there
+    const uint64_t end = __shfl_sync(0xffffffffu, own, lane < V ? 0 : live - 1);
+    const int e = lane & (V - 1);
+    if (lane < 2 * V && (lane < V) == (e < V - m)) at[(lane < V ? 0 : (live - 1) * V) + e] = static_cast<uint8_t>(end >> (8 * e));
 }
 
-template <typename T, int KIND, int NV, bool SHIFT>
+template <typename T, int KIND, bool GROUP, int NV, bool FULL>
 __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutParams p) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     constexpr int E = NV * V;
     constexpr bool QUANT = KIND != kOutSame;
+    constexpr bool GRAW = sizeof(T) == 2 && NV > 2;  // gamma kept in the storage type
+    using Out = typename std::conditional<QUANT, uint8_t, T>::type;
     extern __shared__ __align__(128) unsigned char smem[];
 
     const int tid = threadIdx.x, tpr = p.tpr, W = tpr >> 5, slots = p.slots;
     const int slot = tid / tpr, ts = tid - slot * tpr;
     const int warp = ts >> 5, lane = tid & 31;
     const bool res = QUANT ? p.res != nullptr : true;
-    const bool group = QUANT && p.group;
     const int streams = res ? 2 : 1;
     const bool issuer = warp == 0;
     const int N = p.N, S = p.stages;
     const uint32_t rowb = static_cast<uint32_t>(p.nvec) * 16;
     const int groups = (N + kQuantGroup - 1) / kQuantGroup;
-    const OutLayout L = out_layout(slots, S, streams, p.nvec, SHIFT && group ? groups : 0);
+    const bool meet = GROUP && !FULL && p.across;  // group maxima through shared memory
+    const OutLayout L = out_layout(slots, S, streams, p.nvec, meet ? groups : 0);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar);
     float *reds = reinterpret_cast<float *>(smem + L.red);
     int *flags = reinterpret_cast<int *>(smem + L.flag);
 
-    // this CTA's rows: first + step*i for i < nrows, all of one shift; the
-    // slot's: i = slot + k*slots
-    const int64_t first = blockIdx.x;
-    const int step = p.G;
-    const int nrows = static_cast<int>((p.M - first + step - 1) / step);
-    const int ns = slot < slots && slot < nrows ? (nrows - slot + slots - 1) / slots : 0;
+    // the slot's rows: row + k*row_step for k < ns; a CTA's have one shift
+    const int64_t row_step = (int64_t)p.G * slots, row0 = blockIdx.x * (int64_t)p.cta_step + slot * (int64_t)p.slot_step;
+    int64_t row = row0;
+    const int ns = slot < slots && row < p.M ? static_cast<int>((p.M - row + row_step - 1) / row_step) : 0;
     // the row starts s elements into its first vector; vectors [vb, ve) lie
     // wholly in it
-    const int s = SHIFT ? row_shift(first, p.shift0, p.shift_step, V) : 0;
-    const int nvec = SHIFT ? (s + N + V - 1) / V : p.nvec;
+    const int s = FULL ? 0 : row_shift(blockIdx.x, p.shift0, p.shift_step, V);
+    const int nvec = FULL ? p.nvec : (s + N + V - 1) / V;
     const int vb = s > 0 ? 1 : 0, ve = (s + N) / V;
     // the lane's element beside them, as a place in the staged row: s <= ce < s + N, or -1
     int ce = -1;
-    if (SHIFT && warp == W - 1) {
+    if (!FULL && warp == W - 1) {
         if (lane < V)
             ce = s > 0 && lane >= s && lane < s + N ? lane : -1;
         else if (lane < 2 * V && ve >= vb)
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         fence_barrier_init();
     }
     for (int i = tid; i < slots * 4 * kRedStride; i += kOutThreads) reds[i] = 0.f;
-    if (SHIFT && group)
+    if (meet)
         for (int i = tid; i < slots * 3 * groups; i += kOutThreads) reinterpret_cast<uint32_t *>(smem + L.gmax)[i] = 0;
     if (tid < slots) flags[tid] = 0;
     __syncthreads();
@@ -332,16 +335,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     uint64_t *bar = bars + slot * S;
     const T *base = static_cast<const T *>(lane == 0 || !res ? p.x : p.res);
     const int64_t ld = lane == 0 || !res ? p.ld_x : p.ld_res;
-    const T *src = base + (first + (int64_t)slot * step) * ld - s;
+    const T *src = base + row * ld - s;
     int issued = 0, pst = 0;
-    const int64_t row_step = (int64_t)slots * step;
-    const int64_t src_step = row_step * ld;
     auto issue = [&]() {
         const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
         uint32_t from = 0, to = bytes;
-        unsigned char *dst = ring + ((size_t)pst * streams + lane) * rowb;
-        const int64_t row = SHIFT ? first + slot * (int64_t)step + issued * row_step : 0;
-        if (SHIFT && (row == 0 || row == p.M - 1)) {
+        unsigned char *dst = ring + (pst * streams + lane) * rowb;
+        const int64_t r = FULL ? 1 : row0 + issued * row_step;
+        if (!FULL && (r == 0 || r == p.M - 1)) {
             // the tensors' first and last rows: nothing outside them is read
             if (lane < streams) {
                 if (src < base) from = 16;
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             mbar_arrive_expect_tx(&bar[pst], streams * bytes);
         }
         if (lane < streams && to > from) bulk_load_nohint(dst + from, src + from / sizeof(T), to - from, &bar[pst]);
-        src += src_step;
+        src += row_step * ld;
         if (++pst == S) pst = 0;
         ++issued;
     };
@@ -366,43 +367,56 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
 
     const T *gamma = static_cast<const T *>(p.gamma) - s;  // by place in the staged row
     const bool gvec = (reinterpret_cast<uintptr_t>(gamma) & 15) == 0;
-    float gam[E];
+    float gam[GRAW ? 1 : E];
+    uint4 graw[GRAW ? NV : 1];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = vb + ts + j * tpr;
-        if (v < ve && gvec) {
-            Tr::unpack(ld_global_nc_v4(gamma + v * V), gam + j * V);
+        float g[V];
+        if ((FULL || v < ve) && gvec) {
+            Tr::unpack(ld_global_nc_v4(gamma + v * V), g);
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) gam[j * V + e] = v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
+            for (int e = 0; e < V; ++e) g[e] = FULL || v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
+        }
+        if constexpr (GRAW) {
+            graw[j] = Tr::pack(g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) gam[j * V + e] = g[e];
         }
     }
+    auto gamma_of = [&](int j, float *g) {
+        if constexpr (GRAW) {
+            Tr::unpack(graw[j], g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = gam[j * V + e];
+        }
+    };
     const float ge = ce >= 0 ? Tr::load1(gamma + ce) : 0.f;
 
     const float inv_n = 1.0f / static_cast<float>(N);
-    float *red = reds + (slot < slots ? slot : 0) * 4 * kRedStride;
-    uint32_t *gmax = reinterpret_cast<uint32_t *>(smem + L.gmax) + (slot < slots ? slot : 0) * 3 * groups;
+    const int in_slot = slot < slots ? slot : 0;
+    float *red = reds + in_slot * 4 * kRedStride;
+    uint32_t *gmax = reinterpret_cast<uint32_t *>(smem + L.gmax) + in_slot * 3 * groups;  // of rows k mod 3
     volatile int *flag = flags + slot;
     RingPos pos;
     int buf = 0;  // k mod 3
     int k = 0;
-    int64_t row = first + slot * (int64_t)step;
-    T *h = static_cast<T *>(p.h) + (res ? row * p.ld_h - s : 0);
-    using Out = typename std::conditional<QUANT, uint8_t, T>::type;
-    Out *out = static_cast<Out *>(p.out) + row * p.ld_out - s;
-    const int64_t h_step = row_step * p.ld_h, out_step = row_step * p.ld_out;
-    for (; k < ns; ++k, row += row_step, h += h_step, out += out_step) {
+    for (; k < ns; ++k, row += row_step) {
         const bool timed_out = !mbar_wait_bounded(&bar[pos.stage], pos.parity);
         if (timed_out) record_error(p.err, kErrWaitFull);
-        const unsigned char *sx = ring + (size_t)pos.stage * streams * rowb;
+        const unsigned char *sx = ring + pos.stage * streams * rowb;
         uint32_t *gm = gmax + buf * groups;
+        T *h = static_cast<T *>(p.h) + (res ? row * p.ld_h - s : 0);
         float sum = 0.f, held[E], he = 0.f;
-        uint32_t most = 0, vmost[QUANT ? NV : 1];  // |v| as bits: the order of the values, NaN above all
+        float most = 0.f, vmost[GROUP ? NV : 1];  // max |v|, NaN if any is
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = vb + ts + j * tpr;
-            if constexpr (QUANT) vmost[j] = 0;
-            if (v < ve) {
+            if constexpr (GROUP) vmost[j] = 0.f;
+            if (FULL || v < ve) {
                 float f[V];
                 Tr::unpack(ld_shared_v4(sx + v * 16), f);
                 if (res) {
@@ -414,7 +428,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                         f[2 * i] = t.x, f[2 * i + 1] = t.y;
                     }
                     const uint4 h4 = Tr::pack(f);
-                    st_global_cs_v4(h + (size_t)v * V, h4);
+                    st_global_cs_v4(h + v * V, h4);
                     Tr::unpack(h4, f);
                 }
                 float2 t = pair_mul(pair_at(f, 0), pair_at(f, 0));
@@ -422,41 +436,43 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 for (int i = 1; i < V / 2; ++i) t = pair_fma(pair_at(f, i), pair_at(f, i), t);
                 sum += t.x + t.y;
                 if constexpr (QUANT) {
+                    float g[V];
+                    gamma_of(j, g);
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        const float2 w = pair_mul(pair_at(gam + j * V, i), pair_at(f, i));
+                        const float2 w = pair_mul(pair_at(g, i), pair_at(f, i));
                         held[j * V + 2 * i] = w.x, held[j * V + 2 * i + 1] = w.y;
                     }
                     float m = fabsf(held[j * V]);
 #pragma unroll
                     for (int e = 1; e < V; ++e) m = max_nan(m, fabsf(held[j * V + e]));
-                    vmost[j] = __float_as_uint(m);
-                    if (SHIFT && group) {
-                        const int c0 = v * V - s, split = kQuantGroup - (c0 & (kQuantGroup - 1));
-                        if (split >= V) {
-                            atomicMax(gm + c0 / kQuantGroup, vmost[j]);
-                        } else {
-                            uint32_t m0 = 0, m1 = 0;
+                    if constexpr (GROUP) {
+                        vmost[j] = m;
+                        if (meet) {
+                            const int c0 = v * V - s, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
+                            if (split < V) {  // in two groups
+                                float m1 = m = 0.f;
 #pragma unroll
-                            for (int e = 0; e < V; ++e) {
-                                const uint32_t b = abs_bits(held[j * V + e]);
-                                if (e < split)
-                                    m0 = max(m0, b);
-                                else
-                                    m1 = max(m1, b);
+                                for (int e = 0; e < V; ++e) {
+                                    if (e < split)
+                                        m = max_nan(m, fabsf(held[j * V + e]));
+                                    else
+                                        m1 = max_nan(m1, fabsf(held[j * V + e]));
+                                }
+                                atomicMax(gm + g + 1, __float_as_uint(m1));
                             }
-                            atomicMax(gm + c0 / kQuantGroup, m0);
-                            atomicMax(gm + c0 / kQuantGroup + 1, m1);
+                            atomicMax(gm + g, __float_as_uint(m));
                         }
+                    } else {
+                        most = max_nan(most, m);
                     }
-                    most = max(most, vmost[j]);
                 } else {
 #pragma unroll
                     for (int e = 0; e < V; ++e) held[j * V + e] = f[e];
                 }
             }
         }
-        if (SHIFT && ce >= 0) {
+        if (!FULL && ce >= 0) {
             he = Tr::load1(reinterpret_cast<const T *>(sx) + ce);
             if (res) {
                 he = round_to<T>(he + Tr::load1(reinterpret_cast<const T *>(sx + rowb) + ce));
@@ -465,19 +481,21 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             sum = fmaf(he, he, sum);
             if constexpr (QUANT) {
                 he *= ge;
-                most = max(most, abs_bits(he));
-                if (group) atomicMax(gm + (ce - s) / kQuantGroup, abs_bits(he));
+                most = max_nan(most, fabsf(he));
+                if (meet) atomicMax(gm + (ce - s) / kQuantGroup, abs_bits(he));
             }
         }
-        // the exchange: warp sums (and maxima), added in warp order
+        // the exchange: warp sums (and maxima, as bits: the order of the
+        // values, NaN above all), added in warp order
         sum = warp_sum(sum);
-        if constexpr (QUANT) most = __reduce_max_sync(0xffffffffu, most);
+        uint32_t bits = 0;
+        if constexpr (QUANT && !GROUP) bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
         if (W > 1) {
             float *b = red + (k & 1) * 2 * kRedStride;
             if (timed_out) *flag = 1;
             if (lane == 0) {
                 b[warp] = sum;
-                if constexpr (QUANT) b[kRedStride + warp] = __uint_as_float(most);
+                if constexpr (QUANT && !GROUP) b[kRedStride + warp] = __uint_as_float(bits);
             }
             named_barrier(1 + slot, tpr);
             sum = 0.f;
@@ -487,9 +505,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 sum += t.y;
                 sum += t.z;
                 sum += t.w;
-                if constexpr (QUANT) {
+                if constexpr (QUANT && !GROUP) {
                     const uint4 m = *reinterpret_cast<const uint4 *>(b + kRedStride + w);
-                    most = max(max(max(most, m.x), max(m.y, m.z)), m.w);
+                    bits = max(max(max(bits, m.x), max(m.y, m.z)), m.w);
                 }
             }
             if (*flag) break;
@@ -498,35 +516,45 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             if (__any_sync(0xffffffffu, timed_out)) break;
         }
         // the slot has the row in registers: refill its stage
-        if (issuer && issued < ns) {
+        if (!p.late && issuer && issued < ns) {
             fence_proxy_async();
             issue();
         }
         float rs = 0.f;
-        if (!QUANT || group || ts == 0) rs = __frsqrt_rn(fmaf(sum, inv_n, p.eps));
+        if (!QUANT || GROUP || ts == 0) rs = __frsqrt_rn(fmaf(sum, inv_n, p.eps));
+        if (ts == 0) p.rstd[row] = rs;
+        Out *out = static_cast<Out *>(p.out) + row * p.ld_out - s;
         if constexpr (!QUANT) {
-            T *y = out;
             const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int v = vb + ts + j * tpr;
-                if (v < ve) {
-                    float o[V];
+                if (FULL || v < ve) {
+                    float o[V], g[V];
+                    gamma_of(j, g);
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        const float2 t = pair_mul(pair_at(gam + j * V, i), pair_mul(pair_at(held + j * V, i), rs2));
+                        const float2 t = pair_mul(pair_at(g, i), pair_mul(pair_at(held + j * V, i), rs2));
                         o[2 * i] = t.x, o[2 * i + 1] = t.y;
                     }
-                    st_global_cs_v4(y + (size_t)v * V, Tr::pack(o));
+                    st_global_cs_v4(out + v * V, Tr::pack(o));
                 }
             }
-            if (SHIFT && ce >= 0) Tr::store1(y + ce, ge * (he * rs));
-            if (ts == 0) p.rstd[row] = rs;
+            if (!FULL && ce >= 0) Tr::store1(out + ce, ge * (he * rs));
         } else {
-            uint8_t *q = out;
-            float *scale = p.scale + (group ? row * groups : row);
-            float qf = quant_factor<KIND>(__uint_as_float(most));
-            if (SHIFT && group) {
+            float qf = 0.f;
+            if constexpr (!GROUP) {
+                most = __uint_as_float(bits);
+                qf = quant_factor<KIND>(most);
+                if (ts == 0) p.scale[row] = quant_scale<KIND>(rs, most);
+                if (quant_tiny(most)) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) held[e] *= kRaise;
+                    he *= kRaise;
+                }
+            }
+            float *scale = p.scale + (GROUP ? row * groups : 0);
+            if (meet) {
                 // the maxima of row k-1, read by nobody any more, for row k+2
                 uint32_t *clear = gmax + (buf == 0 ? 2 : buf - 1) * groups;
                 for (int i = ts; i < groups; i += tpr) {
@@ -537,35 +565,42 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int v0 = vb + (ts - lane) + j * tpr, v = v0 + lane;
-                if (v0 >= ve) break;  // the whole warp
+                if (!FULL && v0 >= ve) break;  // the whole warp
                 float *t = held + j * V;
                 uint2 code = make_uint2(0, 0);
-                uint32_t m = most;
-                if (SHIFT && group) {
+                float m = most;
+                if (meet) {
                     // the vector's columns in one group or two
-                    const int c0 = v < ve ? v * V - s : 0, split = kQuantGroup - (c0 & (kQuantGroup - 1));
-                    const uint32_t m0 = gm[c0 / kQuantGroup], m1 = split < V ? gm[c0 / kQuantGroup + 1] : m0;
-                    const float f0 = quant_factor<KIND>(__uint_as_float(m0));
-                    const float f1 = split < V ? quant_factor<KIND>(__uint_as_float(m1)) : f0;
-                    const float r0 = quant_tiny(__uint_as_float(m0)) ? kRaise : 1.f;
-                    const float r1 = quant_tiny(__uint_as_float(m1)) ? kRaise : 1.f;
+                    const int c0 = v < ve ? v * V - s : 0, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
+                    m = __uint_as_float(gm[g]);
+                    const float f0 = quant_factor<KIND>(m), r0 = quant_tiny(m) ? kRaise : 1.f;
+                    float f1 = f0, r1 = r0;
+                    if (split < V) {
+                        const float m1 = __uint_as_float(gm[g + 1]);
+                        f1 = quant_factor<KIND>(m1), r1 = quant_tiny(m1) ? kRaise : 1.f;
+                        m = max_nan(m, m1);
+                    }
 #pragma unroll
                     for (int e = 0; e < V; ++e) t[e] = (t[e] * (e < split ? r0 : r1)) * (e < split ? f0 : f1);
-                    m = max(m0, m1);
                 } else {
-                    if (group) {
+                    if constexpr (GROUP) {
                         // 128 columns: 16 lanes of a 16-bit type, 32 of float32
-                        m = vmost[j];
+                        uint32_t b = __float_as_uint(vmost[j]);
+                        if constexpr (V == 4) {
+                            b = __reduce_max_sync(0xffffffffu, b);
+                        } else {
 #pragma unroll
-                        for (int o = kQuantGroup / V / 2; o > 0; o >>= 1)
-                            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        qf = quant_factor<KIND>(__uint_as_float(m));
-                        if ((lane & (kQuantGroup / V - 1)) == 0 && v < ve)
-                            scale[v * V / kQuantGroup] = quant_scale<KIND>(rs, __uint_as_float(m));
-                    }
-                    if (quant_tiny(__uint_as_float(m))) {
+                            for (int o = kQuantGroup / V / 2; o > 0; o >>= 1)
+                                b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+                        }
+                        m = __uint_as_float(b);
+                        qf = quant_factor<KIND>(m);
+                        if ((lane & (kQuantGroup / V - 1)) == 0 && (FULL || v < ve))
+                            scale[v * V / kQuantGroup] = quant_scale<KIND>(rs, m);
+                        if (quant_tiny(m)) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) t[e] *= kRaise;
+                            for (int e = 0; e < V; ++e) t[e] *= kRaise;
+                        }
                     }
                     const float2 f2 = make_float2(qf, qf);
 #pragma unroll
@@ -574,23 +609,27 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                         t[2 * i] = w.x, t[2 * i + 1] = w.y;
                     }
                 }
-                if (KIND == kOutInt8 && m >= 0x7f800000u) {
+                if (KIND == kOutInt8 && !(m < __int_as_float(0x7f800000))) {
                     code.x = quant4<KIND>(t[0], t[1], t[2], t[3]);
                     if constexpr (V == 8) code.y = quant4<KIND>(t[4], t[5], t[6], t[7]);
                 } else {
                     code.x = quant4_finite<KIND>(t);
                     if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
                 }
-                store_codes<V>(q + (size_t)v0 * V, code, lane, ve - v0 < 32 ? ve - v0 : 32, p.codes_aligned);
+                store_codes<V>(out + v0 * V, code, lane, FULL || ve - v0 > 32 ? 32 : ve - v0, FULL || p.codes_aligned);
             }
-            if (SHIFT && ce >= 0) {
-                const float a = __uint_as_float(group ? gm[(ce - s) / kQuantGroup] : most);
-                q[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
+            if (!FULL && ce >= 0) {
+                if constexpr (GROUP) {
+                    const float a = __uint_as_float(gm[(ce - s) / kQuantGroup]);
+                    out[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
+                } else {
+                    out[ce] = quant1<KIND>(he * qf);
+                }
             }
-            if (ts == 0) {
-                p.rstd[row] = rs;
-                if (!group) *scale = quant_scale<KIND>(rs, __uint_as_float(most));
-            }
+        }
+        if (p.late && issuer && issued < ns) {
+            fence_proxy_async();
+            issue();
         }
         buf = buf == 2 ? 0 : buf + 1;
         pos.next(S);
@@ -607,44 +646,48 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     }
 }
 
-template <typename T, int KIND, int NV, bool SHIFT>
+template <typename T, int KIND, bool GROUP, int NV, bool FULL>
 cudaError_t rms_out_ring_launch(const OutParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, NV, SHIFT>, done);
+    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, GROUP, NV, FULL>, done);
     if (e != cudaSuccess) return e;
-    rms_out_ring_kernel<T, KIND, NV, SHIFT><<<p.G, kOutThreads, smem, s>>>(p);
+    rms_out_ring_kernel<T, KIND, GROUP, NV, FULL><<<p.G, kOutThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, int KIND>
-cudaError_t rms_out_ring_nv(int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
+template <typename T, int KIND, bool GROUP>
+cudaError_t rms_out_ring_nv(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (nv) {
-#define GBN_CASE(n) \
-    case n: return shift ? rms_out_ring_launch<T, KIND, n, true>(p, smem, s) : rms_out_ring_launch<T, KIND, n, false>(p, smem, s)
+#define GBN_CASE(n)                                                               \
+    case n:                                                                       \
+        return full ? rms_out_ring_launch<T, KIND, GROUP, n, true>(p, smem, s)    \
+                    : rms_out_ring_launch<T, KIND, GROUP, n, false>(p, smem, s)
         GBN_CASE(1);
         GBN_CASE(2);
-        GBN_CASE(3);
         GBN_CASE(4);
 #undef GBN_CASE
+        case 3: return rms_out_ring_launch<T, KIND, GROUP, 3, false>(p, smem, s);
         case 6:
+            if constexpr (sizeof(T) == 4) return rms_out_ring_launch<T, KIND, GROUP, 6, false>(p, smem, s);
+            break;
         case 8:
-            if constexpr (sizeof(T) == 4) {
-                if (nv == 6)
-                    return shift ? rms_out_ring_launch<T, KIND, 6, true>(p, smem, s)
-                                 : rms_out_ring_launch<T, KIND, 6, false>(p, smem, s);
-                return shift ? rms_out_ring_launch<T, KIND, 8, true>(p, smem, s)
-                             : rms_out_ring_launch<T, KIND, 8, false>(p, smem, s);
-            }
+            if constexpr (sizeof(T) == 4)
+                return full ? rms_out_ring_launch<T, KIND, GROUP, 8, true>(p, smem, s)
+                            : rms_out_ring_launch<T, KIND, GROUP, 8, false>(p, smem, s);
     }
     return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t rms_out_ring_dispatch(int nv, bool shift, const OutParams &p, size_t smem, cudaStream_t s) {
+cudaError_t rms_out_ring_dispatch(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (p.kind) {
-        case kOutSame: return rms_out_ring_nv<T, kOutSame>(nv, shift, p, smem, s);
-        case kOutE4M3: return rms_out_ring_nv<T, kOutE4M3>(nv, shift, p, smem, s);
-        case kOutInt8: return rms_out_ring_nv<T, kOutInt8>(nv, shift, p, smem, s);
+        case kOutSame: return rms_out_ring_nv<T, kOutSame, false>(nv, full, p, smem, s);
+        case kOutE4M3:
+            return p.group ? rms_out_ring_nv<T, kOutE4M3, true>(nv, full, p, smem, s)
+                           : rms_out_ring_nv<T, kOutE4M3, false>(nv, full, p, smem, s);
+        case kOutInt8:
+            return p.group ? rms_out_ring_nv<T, kOutInt8, true>(nv, full, p, smem, s)
+                           : rms_out_ring_nv<T, kOutInt8, false>(nv, full, p, smem, s);
     }
     return cudaErrorInvalidValue;
 }

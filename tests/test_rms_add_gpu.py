@@ -422,7 +422,7 @@ def test_another_stream_and_a_captured_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y, h, rstd = gbn.rms_add_fwd(d["x"], d["residual"], d["gamma"], EPS)
-        q, scale, _ = gbn.rms_fwd_q8(h, d["gamma"], EPS, group=128)
+        q, scale, rstd_q = gbn.rms_fwd_q8(h, d["gamma"], EPS, group=128)
         dx, dg = gbn.rms_add_bwd(d["dy"], d["dh"], h, d["gamma"], rstd)
     # an eager call of the same inputs between capture and replay
     gbn.rms_add_bwd(d["dy"], d["dh"], h, d["gamma"], torch.ones_like(rstd))
@@ -432,7 +432,7 @@ def test_another_stream_and_a_captured_graph():
         graph.replay()
     torch.cuda.synchronize()
     check_forward(new, y, h, rstd)
-    check_q8(h.cpu(), new["gamma"], q, scale, rstd, 128)
+    check_q8(h.cpu(), new["gamma"], q, scale, rstd_q, 128)
     check_backward(new, h.cpu(), rstd.cpu(), dx, dg)
 
 
