@@ -444,9 +444,10 @@ int rms_add_bwd(const void *dy, const void *dh, const void *h, const void *gamma
  *   norm: one float32 in device memory (out).  workspace: device memory of
  *   gbn_grad_workspace_bytes() bytes, any alignment, its contents on entry
  *   do not matter; two calls that may run at once need one each.
- *   Squares are summed in float32 within 64 bytes a thread and in float64
- *   from there, in a fixed order: the same bits from run to run.  A norm
- *   above the largest float32 is infinity.
+ *   Squares are summed in float32 within 64 bytes a thread and in pairs of
+ *   float32 from there, in a fixed order: the same bits from run to run.
+ *   Squares outside float32's range are scaled first, so every norm that is
+ *   a float32 comes out; one above the largest float32 is infinity.
  *   gbn_grad_clip: out is NULL (in place) or `count` descriptors of the same
  *   n and dtype, none of which overlaps a gradient other than its own and
  *   that one not in part.  A tensor must not be listed twice.  A norm that is

@@ -944,9 +944,9 @@ bool valid_tensors(const gbn_tensor *t, int64_t count) {
     return vecs < (int64_t(1) << 31);
 }
 
-double *grad_partials(void *ws) { return reinterpret_cast<double *>(workspace_partials(ws)); }
+GradSums *grad_partials(void *ws) { return reinterpret_cast<GradSums *>(workspace_partials(ws)); }
 
-size_t grad_workspace(const DevInfo &d) { return (size_t)d.sms * kGradCtasPerSm * sizeof(double) + 256; }
+size_t grad_workspace(const DevInfo &d) { return (size_t)d.sms * kGradCtasPerSm * sizeof(GradSums) + 256; }
 
 }  // namespace
 }  // namespace gbn

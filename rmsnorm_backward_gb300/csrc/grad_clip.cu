@@ -4,18 +4,20 @@
 //   norm = sqrt(sum over all tensors and elements of g^2)
 //   coef = min(1, max_norm / (norm + eps)),  out = round(g * coef)
 //
-// Both kernels walk the same list of 16 KiB chunks; CTA b owns a contiguous
+// Both kernels walk the same list of 32 KiB chunks; CTA b owns a contiguous
 // range of them, so it looks its first tensor up once and then steps.  The
 // table of tensors travels in the launch's parameters: nothing is copied to
 // the device, nothing outlives the call, and a captured launch keeps its
 // own.  Lists longer than a table take several launches.
-//  * norm: a thread squares the 16 bytes x 4 it loads of a chunk in float32
-//    and adds the batch's sum to a double; the CTA's sum goes to its own
-//    double of the workspace, and whoever needs the norm adds those in one
-//    fixed order: no atomics, the same bits from run to run.  A batch whose
-//    float32 sum left the range in which squares keep their precision is
-//    squared again in double from registers, so gradients as small as 1e-38
-//    or as large as 3e38 have their norm.
+//  * norm: a thread squares and adds batches of four 16-byte vectors in
+//    float32 and gathers the batches' sums as a float32 pair (a sum and what
+//    its roundings lost), which holds some 48 bits: sm_103a adds doubles at a
+//    64th of that rate, and the doubles of one CTA's last reduction took as
+//    long as a megabyte.  Batches whose squares would leave float32's range
+//    are scaled by a power of two first and gathered apart, so gradients as
+//    small as 1e-38 or as large as 3e38 have their norm.  The CTA's sums go to
+//    its own place in the workspace, and whoever needs the norm adds those in
+//    one fixed order: no atomics, the same bits from run to run.
 //  * clip: every CTA forms coef from the partial sums itself (no kernel in
 //    between), then walks its chunks backwards: what the first pass read
 //    last is still in L2.  In place with coef = 1 there is nothing to do.
@@ -38,7 +40,7 @@ struct GradEntry {
 template <int CAP>
 struct GradTable {
     GradEntry e[CAP];
-    double *partial;
+    GradSums *partial;
     float *norm;
     uint32_t chunks;  // in this launch
     int count;
@@ -62,23 +64,82 @@ inline int64_t chunks_of(const gbn_tensor &t) {
     return c > 0 ? c : 1;
 }
 
-// sum of a batch's squares in double, from its raw vectors
+// A float32 sum and what its roundings lost (Knuth's two-sum).
+struct Pair {
+    float hi = 0.f, lo = 0.f;
+};
+__device__ __forceinline__ void add(Pair &p, float b) {
+    const float s = __fadd_rn(p.hi, b), bb = __fsub_rn(s, p.hi);
+    p.lo += __fadd_rn(__fsub_rn(p.hi, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+    p.hi = s;
+}
+__device__ __forceinline__ void add(Pair &p, const Pair &q) {
+    add(p, q.hi);
+    p.lo += q.lo;
+}
+
+// A thread's sums of squares: of x, of x * 2^-80 where a batch's sum is above
+// 2^60 (or not finite), of x * 2^80 where it is below 2^-80.  Squares from
+// there on are normal float32 values or negligible in their batch, and the
+// sums stay in range for 2^34 batches.
+constexpr float kBatchMost = 0x1p60f, kBatchLeast = 0x1p-80f;
+struct Sums {
+    Pair mid;
+    float big = 0.f, small = 0.f;
+};
+
 template <typename T>
-__device__ __noinline__ double slow_squares(uint4 v0, uint4 v1, uint4 v2, uint4 v3) {
-    const uint4 v[kGradVecs] = {v0, v1, v2, v3};
-    double d = 0.0;
+__device__ __forceinline__ float sum_squares(const uint4 (&raw)[4], float scale) {
+    constexpr int V = Traits<T>::kVec;
+    float s[4];
 #pragma unroll
-    for (int j = 0; j < kGradVecs; ++j) {
-        float f[Traits<T>::kVec];
-        Traits<T>::unpack(v[j], f);
+    for (int j = 0; j < 4; ++j) {
+        float f[V];
+        Traits<T>::unpack(raw[j], f);
+        if (scale != 1.f) {
 #pragma unroll
-        for (int e = 0; e < Traits<T>::kVec; ++e) d += static_cast<double>(f[e]) * static_cast<double>(f[e]);
+            for (int e = 0; e < V; ++e) f[e] *= scale;
+        }
+        s[j] = f[0] * f[0];
+#pragma unroll
+        for (int e = 1; e < V; ++e) s[j] = fmaf(f[e], f[e], s[j]);
     }
-    return d;
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const GradEntry &t, uint32_t chunk) {
+__device__ __noinline__ float scaled_squares(uint4 v0, uint4 v1, uint4 v2, uint4 v3, float scale) {
+    const uint4 raw[4] = {v0, v1, v2, v3};
+    return sum_squares<T>(raw, scale);
+}
+
+template <typename T>
+__device__ __forceinline__ void add_batch(Sums &sums, const uint4 (&raw)[4]) {
+    const float b = sum_squares<T>(raw, 1.f);
+    if (b >= kBatchLeast && b <= kBatchMost) {
+        add(sums.mid, b);
+    } else if (b < kBatchLeast) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= raw[j].x | raw[j].y | raw[j].z | raw[j].w;
+        if (any) sums.small += scaled_squares<T>(raw[0], raw[1], raw[2], raw[3], 0x1p80f);
+    } else {
+        sums.big += scaled_squares<T>(raw[0], raw[1], raw[2], raw[3], 0x1p-80f);
+    }
+}
+
+__device__ __forceinline__ void add_one(Sums &sums, float f) {
+    const float b = f * f;
+    if (b >= kBatchLeast && b <= kBatchMost)
+        add(sums.mid, b);
+    else if (b < kBatchLeast)
+        sums.small += (f * 0x1p80f) * (f * 0x1p80f);
+    else
+        sums.big += (f * 0x1p-80f) * (f * 0x1p-80f);
+}
+
+template <typename T>
+__device__ __forceinline__ void add_chunk(Sums &sums, const GradEntry &t, uint32_t chunk) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     const T *src = static_cast<const T *>(t.src);
@@ -86,56 +147,46 @@ __device__ __forceinline__ double chunk_squares(const GradEntry &t, uint32_t chu
     const int64_t nvec = (t.n - head) / V;
     const T *body = src + head;
     const int64_t v0 = static_cast<int64_t>(chunk) * kGradChunkVecs + threadIdx.x;
-    uint4 raw[kGradVecs];
+    uint4 raw[kGradVecs / 4][4];
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
         const int64_t v = v0 + j * kGradThreads;
-        raw[j] = v < nvec ? ld_global_nc_v4(body + v * V) : make_uint4(0, 0, 0, 0);
+        raw[j / 4][j % 4] = v < nvec ? ld_global_nc_v4(body + v * V) : make_uint4(0, 0, 0, 0);
     }
-    double extra = 0.0;
     if (chunk == 0) {  // the elements before and after the 16-byte vectors
         const int64_t tail = t.n - head - nvec * V;
-        if (threadIdx.x < head) {
-            const double f = Tr::load1(src + threadIdx.x);
-            extra += f * f;
-        }
-        if (threadIdx.x < tail) {
-            const double f = Tr::load1(body + nvec * V + threadIdx.x);
-            extra += f * f;
-        }
+        if (threadIdx.x < head) add_one(sums, Tr::load1(src + threadIdx.x));
+        if (threadIdx.x < tail) add_one(sums, Tr::load1(body + nvec * V + threadIdx.x));
     }
-    float s[kGradVecs];
 #pragma unroll
-    for (int j = 0; j < kGradVecs; ++j) {
-        float f[V];
-        Tr::unpack(raw[j], f);
-        s[j] = f[0] * f[0];
-#pragma unroll
-        for (int e = 1; e < V; ++e) s[j] = fmaf(f[e], f[e], s[j]);
-    }
-    static_assert(kGradVecs == 4, "the sum below");
-    const float b = (s[0] + s[1]) + (s[2] + s[3]);
-    // squares below 2^-126 lose bits, above 2^128 they overflow
-    if (!(b >= 0x1p-80f && b <= 0x1p100f)) {
-        uint32_t any = 0;
-#pragma unroll
-        for (int j = 0; j < kGradVecs; ++j) any |= raw[j].x | raw[j].y | raw[j].z | raw[j].w;
-        if (any) return extra + slow_squares<T>(raw[0], raw[1], raw[2], raw[3]);
-    }
-    return extra + static_cast<double>(b);
+    for (int j = 0; j < kGradVecs / 4; ++j) add_batch<T>(sums, raw[j]);
 }
 
-// sum over the CTA in a fixed order; every thread gets it
-__device__ __forceinline__ double cta_sum(double v, double *sm) {
+// The CTA's sums in a fixed order, on every thread; sm holds 4 floats a warp.
+__device__ __forceinline__ Sums cta_sum(Sums v, float4 *sm) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    for (int o = 16; o > 0; o >>= 1) {
+        Pair q;
+        q.hi = __shfl_xor_sync(0xffffffffu, v.mid.hi, o);
+        q.lo = __shfl_xor_sync(0xffffffffu, v.mid.lo, o);
+        add(v.mid, q);
+        v.big += __shfl_xor_sync(0xffffffffu, v.big, o);
+        v.small += __shfl_xor_sync(0xffffffffu, v.small, o);
+    }
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float4(v.mid.hi, v.mid.lo, v.big, v.small);
     __syncthreads();
-    v = sm[0];
+    Sums s;
 #pragma unroll
-    for (int w = 1; w < kGradThreads / 32; ++w) v += sm[w];
+    for (int w = 0; w < kGradThreads / 32; ++w) {
+        const float4 q = sm[w];
+        Pair m;
+        m.hi = q.x, m.lo = q.y;
+        add(s.mid, m);
+        s.big += q.z;
+        s.small += q.w;
+    }
     __syncthreads();
-    return v;
+    return s;
 }
 
 // this CTA's chunks [c0, c1)
@@ -161,13 +212,17 @@ __device__ __forceinline__ int find_entry(const GradTable<CAP> &t, uint32_t c) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ double sm[kGradThreads / 32];
+__global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t) {
+    __shared__ float4 sm[kGradThreads / 32];
     // the gradients, and whoever still reads the partial sums, come before
     // this kernel on the stream; the clip may launch meanwhile and waits
     griddep_wait();
     griddep_launch_dependents();
-    double sum = 0.0;
+    Sums sums;
+    if (t.add && threadIdx.x == 0) {  // a later launch of the same list
+        const GradSums p = t.partial[blockIdx.x];
+        sums.mid.hi = p.hi, sums.mid.lo = p.lo, sums.big = p.big, sums.small = p.small;
+    }
     uint32_t c, c1;
     cta_range(t.chunks, c, c1);
     if (c < c1) {
@@ -176,60 +231,84 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
             while (i + 1 < t.count && t.e[i + 1].first <= c) ++i;
             const GradEntry &e = t.e[i];
             const uint32_t k = c - e.first;
-            sum += e.dtype == GBN_F32   ? chunk_squares<float>(e, k)
-                   : e.dtype == GBN_F16 ? chunk_squares<__half>(e, k)
-                                        : chunk_squares<__nv_bfloat16>(e, k);
+            if (e.dtype == GBN_F32)
+                add_chunk<float>(sums, e, k);
+            else if (e.dtype == GBN_F16)
+                add_chunk<__half>(sums, e, k);
+            else
+                add_chunk<__nv_bfloat16>(sums, e, k);
         }
     }
-    sum = cta_sum(sum, sm);
-    if (threadIdx.x == 0) t.partial[blockIdx.x] = t.add ? t.partial[blockIdx.x] + sum : sum;
+    sums = cta_sum(sums, sm);
+    if (threadIdx.x == 0) t.partial[blockIdx.x] = GradSums{sums.mid.hi, sums.mid.lo, sums.big, sums.small};
 }
 
-// the norm from the CTAs' sums, in a fixed order
-__device__ __forceinline__ double norm_of(const double *partial, int total, double *sm) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < total; i += kGradThreads) v += __ldcg(partial + i);
-    return sqrt(cta_sum(v, sm));
+// The norm from the CTAs' sums, in a fixed order: the float32 root of the
+// pair, improved by one step of Newton's method from the pair's residual, or
+// a float64 root where some batches were scaled or the sum is zero, infinite
+// or NaN (a norm above the largest float32 is infinite).
+__device__ __forceinline__ float norm_of(const GradSums *partial, int total, float4 *sm) {
+    Sums v;
+    for (int i = threadIdx.x; i < total; i += kGradThreads) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(partial + i));
+        Pair m;
+        m.hi = q.x, m.lo = q.y;
+        add(v.mid, m);
+        v.big += q.z;
+        v.small += q.w;
+    }
+    v = cta_sum(v, sm);
+    if (v.big == 0.f && v.small == 0.f && v.mid.hi >= 0x1p-100f && v.mid.hi <= 0x1p120f) {
+        const float r = sqrtf(v.mid.hi);
+        return r + (fmaf(-r, r, v.mid.hi) + v.mid.lo) / (2.f * r);
+    }
+    const double d = static_cast<double>(v.mid.hi) + static_cast<double>(v.mid.lo) +
+                     static_cast<double>(v.big) * 0x1p160 + static_cast<double>(v.small) * 0x1p-160;
+    return static_cast<float>(sqrt(d));
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_norm_finish_kernel(const double *partial, int total,
+__global__ void __launch_bounds__(kGradThreads) grad_norm_finish_kernel(const GradSums *partial, int total,
                                                                        float *norm) {
-    __shared__ double sm[kGradThreads / 32];
+    __shared__ float4 sm[kGradThreads / 32];
     griddep_wait();
-    const double n = norm_of(partial, total, sm);
-    if (threadIdx.x == 0) *norm = static_cast<float>(n);
+    const float n = norm_of(partial, total, sm);
+    if (threadIdx.x == 0) *norm = n;
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const GradEntry &t, uint32_t chunk, float coef) {
+__device__ __forceinline__ void scale_chunk(const GradEntry &t, uint32_t chunk, float coef) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     const T *src = static_cast<const T *>(t.src);
     T *dst = static_cast<T *>(t.dst);
     const int64_t head = head_of<T>(src, t.n);
     const int64_t nvec = (t.n - head) / V;
-    const int64_t v0 = static_cast<int64_t>(chunk) * kGradChunkVecs + threadIdx.x;
     const bool same = (reinterpret_cast<uintptr_t>(dst + head) & 15) == 0;
-    uint4 raw[kGradVecs];
+    // four vectors at a time: registers for four CTAs on an SM
+#pragma unroll 1
+    for (int64_t v0 = (int64_t)chunk * kGradChunkVecs + threadIdx.x, end = v0 + kGradChunkVecs; v0 < end;
+         v0 += 4 * kGradThreads) {
+        uint4 raw[4];
 #pragma unroll
-    for (int j = 0; j < kGradVecs; ++j) {
-        const int64_t v = v0 + j * kGradThreads;
-        if (v < nvec) raw[j] = *reinterpret_cast<const uint4 *>(src + head + v * V);
-    }
+        for (int j = 0; j < 4; ++j) {
+            const int64_t v = v0 + j * kGradThreads;
+            if (v < nvec) raw[j] = __ldcg(reinterpret_cast<const uint4 *>(src + head + v * V));
+        }
 #pragma unroll
-    for (int j = 0; j < kGradVecs; ++j) {
-        const int64_t v = v0 + j * kGradThreads;
-        if (v < nvec) {
-            float f[V];
-            Tr::unpack(raw[j], f);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t v = v0 + j * kGradThreads;
+            if (v < nvec) {
+                float f[V];
+                Tr::unpack(raw[j], f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] *= coef;
-            T *d = dst + head + v * V;
-            if (same) {
-                *reinterpret_cast<uint4 *>(d) = Tr::pack(f);
-            } else {
+                for (int e = 0; e < V; ++e) f[e] *= coef;
+                T *d = dst + head + v * V;
+                if (same) {
+                    st_global_cs_v4(d, Tr::pack(f));
+                } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) Tr::store1(d + e, f[e]);
+                    for (int e = 0; e < V; ++e) Tr::store1(d + e, f[e]);
+                }
             }
         }
     }
@@ -241,13 +320,13 @@ __device__ __forceinline__ void chunk_scale(const GradEntry &t, uint32_t chunk, 
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ double sm[kGradThreads / 32];
+__global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_clip_kernel(const __grid_constant__ GradTable<CAP> t) {
+    __shared__ float4 sm[kGradThreads / 32];
     griddep_wait();
-    const double norm = norm_of(t.partial, t.total, sm);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && !t.add) *t.norm = static_cast<float>(norm);
-    const double c = static_cast<double>(t.max_norm) / (norm + static_cast<double>(t.eps));
-    const float coef = c >= 1.0 ? 1.f : static_cast<float>(c);  // NaN stays NaN
+    const float norm = norm_of(t.partial, t.total, sm);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && !t.add) *t.norm = norm;
+    const float c = t.max_norm / (norm + t.eps);
+    const float coef = c >= 1.f ? 1.f : c;  // NaN stays NaN
     uint32_t c0, k;
     cta_range(t.chunks, c0, k);
     if (c0 >= k) return;
@@ -258,11 +337,11 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
         if (coef == 1.f && e.src == e.dst) continue;
         const uint32_t at = k - e.first;
         if (e.dtype == GBN_F32)
-            chunk_scale<float>(e, at, coef);
+            scale_chunk<float>(e, at, coef);
         else if (e.dtype == GBN_F16)
-            chunk_scale<__half>(e, at, coef);
+            scale_chunk<__half>(e, at, coef);
         else
-            chunk_scale<__nv_bfloat16>(e, at, coef);
+            scale_chunk<__nv_bfloat16>(e, at, coef);
     }
 }
 
@@ -283,7 +362,7 @@ cudaError_t launch_pdl(K kernel, int grid, cudaStream_t s, const P &p) {
 // One pass over the list: tables of up to CAP tensors, a launch for each.
 template <int CAP>
 cudaError_t run_list(const gbn_tensor *g, const gbn_tensor *out, int64_t count, bool clip, int grid, float max_norm,
-                     float eps, float *norm, double *partial, cudaStream_t s) {
+                     float eps, float *norm, GradSums *partial, cudaStream_t s) {
     GradTable<CAP> t;
     t.partial = partial;
     t.norm = norm;
@@ -316,7 +395,7 @@ cudaError_t run_list(const gbn_tensor *g, const gbn_tensor *out, int64_t count, 
 }
 
 cudaError_t run_any(const gbn_tensor *g, const gbn_tensor *out, int64_t count, bool clip, int grid, float max_norm,
-                    float eps, float *norm, double *partial, cudaStream_t s) {
+                    float eps, float *norm, GradSums *partial, cudaStream_t s) {
     return count <= kSmallTable
                ? run_list<kSmallTable>(g, out, count, clip, grid, max_norm, eps, norm, partial, s)
                : run_list<kLargeTable>(g, out, count, clip, grid, max_norm, eps, norm, partial, s);
@@ -330,7 +409,7 @@ int grid_of(const gbn_tensor *g, int64_t count, int sms) {
 
 }  // namespace
 
-cudaError_t launch_grad_norm(const gbn_tensor *g, int64_t count, float *norm, double *partial, int sms,
+cudaError_t launch_grad_norm(const gbn_tensor *g, int64_t count, float *norm, GradSums *partial, int sms,
                              cudaStream_t s) {
     const int grid = grid_of(g, count, sms);
     cudaError_t e = run_any(g, nullptr, count, false, grid, 0.f, 0.f, norm, partial, s);
@@ -344,11 +423,11 @@ cudaError_t launch_grad_norm(const gbn_tensor *g, int64_t count, float *norm, do
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const double *>(partial), grid, norm);
+    return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel, static_cast<const GradSums *>(partial), grid, norm);
 }
 
 cudaError_t launch_grad_clip(const gbn_tensor *g, const gbn_tensor *out, int64_t count, float max_norm, float eps,
-                             float *norm, double *partial, int sms, cudaStream_t s) {
+                             float *norm, GradSums *partial, int sms, cudaStream_t s) {
     const int grid = grid_of(g, count, sms);
     const cudaError_t e = run_any(g, nullptr, count, false, grid, 0.f, 0.f, norm, partial, s);
     if (e != cudaSuccess) return e;
