@@ -442,6 +442,10 @@ def gelu_bwd(dy: torch.Tensor, preact: torch.Tensor, *, dx: Optional[torch.Tenso
 # RMSNorm with the residual's addition and / or an 8-bit output, its backward
 # ---------------------------------------------------------------------------
 _ROW_KERNELS = {"auto": 0, "plain": 2}
+# the current stream's handle without a Stream object, where torch has it: a
+# call on a few rows costs the host more than the GPU, and the object alone
+# 1.9 of 13.5 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _enqueue(fn: str, device, stream, args, owned=()) -> None:
@@ -449,12 +453,16 @@ def _enqueue(fn: str, device, stream, args, owned=()) -> None:
     owned: tensors allocated for this call; where it runs on another stream
     than the one they were allocated on, their memory stays theirs until that
     stream is done with it."""
-    call = getattr(lib(), fn)
+    call = getattr(_lib or lib(), fn)
+    if stream is not None or _raw_stream is None:
+        handle = _stream(device, stream)
+    else:
+        handle = _raw_stream(device.index)
     if torch.cuda.current_device() == device.index:
-        status = call(*args, _stream(device, stream))
+        status = call(*args, handle)
     else:
         with torch.cuda.device(device):
-            status = call(*args, _stream(device, stream))
+            status = call(*args, handle)
     if status != GBN_OK:
         raise GbnError(fn, status)
     if stream is not None and owned:
@@ -464,23 +472,16 @@ def _enqueue(fn: str, device, stream, args, owned=()) -> None:
             t.record_stream(stream)
 
 
-def _out_rows(t: Optional[torch.Tensor], name: str, shape, dtype, device, owned) -> Tuple[torch.Tensor, int]:
-    """An output of ``shape`` (allocated if None) and its row stride."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        owned.append(t)
-        return t, shape[-1]
+def _rows_like(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """Row stride of t, which must have this shape, dtype and device."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t, _rows_ld(t, name)[2]
+    return shape[-1] if t.is_contiguous() else _rows_ld(t, name)[2]
 
 
-def _out_vec(t: Optional[torch.Tensor], name: str, n: int, device, owned) -> torch.Tensor:
-    if t is None:
-        t = torch.empty(n, dtype=torch.float32, device=device)
-        owned.append(t)
-    else:
-        _vec(t, name, n, torch.float32, device)
+def _new(shape, dtype, device, owned) -> torch.Tensor:
+    t = torch.empty(shape, dtype=dtype, device=device)
+    owned.append(t)
     return t
 
 
@@ -494,32 +495,33 @@ def rms_add_fwd(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, ep
     Row tensors may be 2-D views with contiguous rows.  kernel: "auto" or
     "plain"."""
     M, N, ld_x = _rows_ld(x, "x")
-    device, owned = x.device, []
-    ld_r = _same_rows(residual, x, "residual")
-    _vec(gamma, "gamma", N, x.dtype, device)
-    y, ld_y = _out_rows(y, "y", x.shape, x.dtype, device, owned)
-    h, ld_h = _out_rows(h, "h", x.shape, x.dtype, device, owned)
-    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    shape, dtype, device, owned = x.shape, x.dtype, x.device, []
+    ld_r = _rows_like(residual, "residual", shape, dtype, device)
+    _vec(gamma, "gamma", N, dtype, device)
+    y = _new(shape, dtype, device, owned) if y is None else y
+    h = _new(shape, dtype, device, owned) if h is None else h
+    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
+    ld_y, ld_h = _rows_like(y, "y", shape, dtype, device), _rows_like(h, "h", shape, dtype, device)
+    _vec(rstd, "rstd", M, torch.float32, device)
     _enqueue("rms_add_fwd", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), y.data_ptr(), h.data_ptr(), rstd.data_ptr(),
               eps, M, N, _code(x), ld_x, ld_r, ld_y, ld_h, _ROW_KERNELS[kernel]), owned)
     return y, h, rstd
 
 
-def _q8_args(x, N, q_dtype, group, q, scale, M, owned):
+def _q8_args(shape, device, q_dtype, group, q, scale, owned):
     if q is not None:
         q_dtype = q.dtype
     if q_dtype not in Q_DTYPE_CODES:
         raise ValueError(f"q_dtype must be one of {sorted(map(str, Q_DTYPE_CODES))}")
-    if group not in (0, QUANT_GROUP):
+    if group != 0 and group != QUANT_GROUP:
         raise ValueError(f"group must be 0 (a scale for each row) or {QUANT_GROUP}")
-    q, ld_q = _out_rows(q, "q", x.shape, q_dtype, x.device, owned)
-    shape = x.shape[:-1] + ((N + QUANT_GROUP - 1) // QUANT_GROUP,) if group else x.shape[:-1]
-    if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-        owned.append(scale)
-    elif scale.dtype != torch.float32 or scale.shape != shape or not scale.is_contiguous() or scale.device != x.device:
-        raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(shape)} on {x.device}")
+    q = _new(shape, q_dtype, device, owned) if q is None else q
+    ld_q = _rows_like(q, "q", shape, q_dtype, device)
+    scales = shape[:-1] + ((shape[-1] + QUANT_GROUP - 1) // QUANT_GROUP,) if group else shape[:-1]
+    scale = _new(scales, torch.float32, device, owned) if scale is None else scale
+    if scale.shape != scales or scale.dtype != torch.float32 or scale.device != device or not scale.is_contiguous():
+        raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(scales)} on {device}")
     return q, ld_q, scale, Q_DTYPE_CODES[q_dtype]
 
 
@@ -535,8 +537,9 @@ def rms_fwd_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, q_dtype=torc
     M, N, ld_x = _rows_ld(x, "x")
     device, owned = x.device, []
     _vec(gamma, "gamma", N, x.dtype, device)
-    q, ld_q, scale, q_code = _q8_args(x, N, q_dtype, group, q, scale, M, owned)
-    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    q, ld_q, scale, q_code = _q8_args(x.shape, device, q_dtype, group, q, scale, owned)
+    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
+    _vec(rstd, "rstd", M, torch.float32, device)
     _enqueue("rms_fwd_q8", device, stream,
              (x.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), eps, M, N, _code(x),
               q_code, group, ld_x, ld_q, _ROW_KERNELS[kernel]), owned)
@@ -551,12 +554,14 @@ def rms_add_fwd_q8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
 
     h as in rms_add_fwd (it may be x or residual), the rest as in rms_fwd_q8."""
     M, N, ld_x = _rows_ld(x, "x")
-    device, owned = x.device, []
-    ld_r = _same_rows(residual, x, "residual")
-    _vec(gamma, "gamma", N, x.dtype, device)
-    q, ld_q, scale, q_code = _q8_args(x, N, q_dtype, group, q, scale, M, owned)
-    h, ld_h = _out_rows(h, "h", x.shape, x.dtype, device, owned)
-    rstd = _out_vec(rstd, "rstd", M, device, owned)
+    shape, dtype, device, owned = x.shape, x.dtype, x.device, []
+    ld_r = _rows_like(residual, "residual", shape, dtype, device)
+    _vec(gamma, "gamma", N, dtype, device)
+    q, ld_q, scale, q_code = _q8_args(shape, device, q_dtype, group, q, scale, owned)
+    h = _new(shape, dtype, device, owned) if h is None else h
+    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
+    ld_h = _rows_like(h, "h", shape, dtype, device)
+    _vec(rstd, "rstd", M, torch.float32, device)
     _enqueue("rms_add_fwd_q8", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), h.data_ptr(),
               rstd.data_ptr(), eps, M, N, _code(x), q_code, group, ld_x, ld_r, ld_q, ld_h, _ROW_KERNELS[kernel]),
@@ -574,31 +579,31 @@ def rms_add_bwd(dy: torch.Tensor, dh: torch.Tensor, h: torch.Tensor, gamma: torc
     may be dy, dh or h, is the gradient of x and of residual alike.  dgamma,
     accumulate, grad_dtype and workspace as for rms_bwd; kernel: "auto" or
     "plain"."""
-    if grad_dtype not in (torch.float32, h.dtype):
-        raise ValueError("grad_dtype must be float32 or h's dtype")
     M, N, ld_h = _rows_ld(h, "h")
-    device, owned = h.device, []
-    ld_dy = _same_rows(dy, h, "dy")
-    ld_dh = _same_rows(dh, h, "dh")
-    _vec(gamma, "gamma", N, h.dtype, device)
+    shape, dtype, device, owned = h.shape, h.dtype, h.device, []
+    if grad_dtype != torch.float32 and grad_dtype != dtype:
+        raise ValueError("grad_dtype must be float32 or h's dtype")
+    ld_dy, ld_dh = _rows_like(dy, "dy", shape, dtype, device), _rows_like(dh, "dh", shape, dtype, device)
+    _vec(gamma, "gamma", N, dtype, device)
     _vec(rstd, "rstd", M, torch.float32, device)
-    dx, ld_dx = _out_rows(dx, "dx", h.shape, h.dtype, device, owned)
+    dx = _new(shape, dtype, device, owned) if dx is None else dx
+    ld_dx = _rows_like(dx, "dx", shape, dtype, device)
     if dgamma is None:
         dgamma = _grads(None, "dgamma", N, grad_dtype, device, accumulate)
         owned.append(dgamma)
     else:
         _vec(dgamma, "dgamma", N, grad_dtype, device)
     if workspace is None:
-        workspace = torch.empty(max(bwd_workspace_bytes(M, N, h.dtype, False, device), 1), dtype=torch.uint8,
-                                device=device)
-        owned.append(workspace)
+        workspace = _new(max(bwd_workspace_bytes(M, N, dtype, False, device), 1), torch.uint8, device, owned)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on h's device")
-    opt = GbnOptions(ld_h, ld_dy, ld_dx, 1 if accumulate else 0, DTYPE_CODES[grad_dtype], 0, _ROW_KERNELS[kernel], 0, 0)
+    opt = None
+    if accumulate or kernel != "auto" or grad_dtype != torch.float32 or not ld_h == ld_dy == ld_dx == N:
+        opt = ctypes.byref(GbnOptions(ld_h, ld_dy, ld_dx, 1 if accumulate else 0, DTYPE_CODES[grad_dtype], 0,
+                                      _ROW_KERNELS[kernel], 0, 0))
     _enqueue("rms_add_bwd", device, stream,
              (dy.data_ptr(), dh.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-              dgamma.data_ptr(), M, N, _code(h), workspace.data_ptr(), workspace.nbytes, ld_dh, ctypes.byref(opt)),
-             owned)
+              dgamma.data_ptr(), M, N, _code(h), workspace.data_ptr(), workspace.nbytes, ld_dh, opt), owned)
     return dx, dgamma
 
 
