@@ -775,9 +775,11 @@ bool valid_eps(float eps) { return eps >= 0.f && isfinite(eps); }
 // tensors' rows lie alike to 16-byte boundaries and two stages of a row fit;
 // fills the kernel's fields of p.
 struct OutPlan {
-    bool ok = false, full = false;
-    int nv = 0;
+    bool ok = false;
+    int nv = 0, lie = 0;
     size_t smem = 0;
+    // short rows: how rows lie, and no ring plan
+    bool short_rows = false, vec = false;
 };
 
 OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
@@ -787,9 +789,20 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     const RowBase res = p->res ? RowBase{p->res, p->ld_res} : x, h = p->res ? RowBase{p->h, p->ld_h} : x;
     const RowBase out = p->kind == kOutSame ? RowBase{p->out, p->ld_out} : x;
     const RowPhases r = row_phases(es, p->M, p->N, {x, res, h, out});
+    p->codes_aligned = reinterpret_cast<uintptr_t>(p->out) % V == 0 && p->ld_out % V == 0;
+    const bool whole = r.ok && !r.shift && (p->kind == kOutSame || p->codes_aligned);
+    // short rows; element by element and without codes to make, the ring
+    // overtakes on many rows (bf16, 32000x255: 17.5 us here, 17.1 there;
+    // 32000x511: 42.7, 25.0; 100x255: 2.2, 3.8; to e4m3, 32000x255: 17.5, 20.7)
+    const bool many = p->kind == kOutSame && p->M > (int64_t)32 * d.sms;
+    if (whole ? p->N <= kShortVectors * V : p->N <= (many ? kShortElements / 2 : kShortElements)) {
+        P.short_rows = true;
+        P.vec = whole;
+        return P;
+    }
     const int G = phase_grid(p->M, r.phases, d, d.sms);
     if (!r.ok || G < 1 || p->M / G >= (1 << 30)) return P;
-    const int groups = r.shift && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
+    const int groups = !whole && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
     // without a residual to read, the row's work next to its bytes is more, and
     // more vectors a thread spread what a row costs besides them (e4m3,
     // 16384x4096 bf16: 2 52 us, 4 40 us)
@@ -802,8 +815,7 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     p->G = G;
     p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec;
     p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
-    p->codes_aligned = r.shift0 == 0 && r.step == 0 && reinterpret_cast<uintptr_t>(p->out) % V == 0 && p->ld_out % V == 0;
-    p->across = r.shift;
+    if (r.shift0 != 0 || r.step != 0) p->codes_aligned = 0;
     // wide rows: two stages already are more in flight than HBM likes beside
     // the writes, so a stage is refilled after its row's stores (8192x16384
     // bf16 to e4m3 by 128 columns: 157.6 us before them, 142.9 after; on
@@ -814,7 +826,8 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     const bool near = !r.shift && p->M >= (int64_t)4 * G * s.slots;
     p->cta_step = near ? s.slots : 1;
     p->slot_step = near ? 1 : G;
-    P.ok = true, P.full = !r.shift && r.nvec == s.nv * s.tpr && s.nv != 3 && s.nv != 6 && (p->kind == kOutSame || p->codes_aligned), P.nv = s.nv;
+    P.ok = true, P.nv = s.nv;
+    P.lie = !whole ? kLieAcross : r.nvec == s.nv * s.tpr && (s.nv & (s.nv - 1)) == 0 ? kLieFull : kLieWhole;
     P.smem = out_layout(s.slots, s.stages, streams, r.nvec, groups).total;
     return P;
 }
@@ -850,10 +863,12 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     p.x = x; p.res = has_res ? res : nullptr; p.gamma = gamma; p.h = has_res ? h : nullptr; p.out = out;
     p.rstd = rstd; p.scale = scale; p.eps = eps; p.M = M; p.N = static_cast<int>(N);
     p.ld_x = ld_x; p.ld_res = ld_res; p.ld_h = ld_h; p.ld_out = ld_out;
-    p.kind = kind; p.group = group != 0; p.err = d.err;
+    p.kind = kind; p.group = group != 0 && N > kQuantGroup; p.err = d.err;  // one group is a row
+   
     if (kernel == GBN_KERNEL_AUTO) {
         const OutPlan P = out_plan(dtype, d, &p);
-        if (P.ok) return cuda_status(launch_rms_out_ring(dtype, P.nv, P.full, p, P.smem, stream));
+        if (P.short_rows) return cuda_status(launch_rms_out_short(dtype, P.vec, p, d.sms, stream));
+        if (P.ok) return cuda_status(launch_rms_out_ring(dtype, P.nv, P.lie, p, P.smem, stream));
     }
     return cuda_status(launch_rms_out_plain(dtype, kind, group != 0, p, d.sms, stream));
 }
@@ -864,7 +879,7 @@ int out_kind(int q_dtype) { return q_dtype == GBN_E4M3 ? kOutE4M3 : q_dtype == G
 // lie alike to 16-byte boundaries and two stages of a row fit; fills the
 // kernel's fields of p (and G, which the phases may lower).
 struct AddBwdPlan {
-    bool ok = false, shift = false;
+    bool ok = false, shift = false, short_rows = false, vec = false;
     int nv = 0;
     size_t smem = 0;
 };
@@ -874,6 +889,17 @@ AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
     const int es = elem_bytes(dtype), V = 16 / es;
     const RowPhases r =
         row_phases(es, p->M, p->N, {{p->h, p->ld_h}, {p->dy, p->ld_dy}, {p->dh, p->ld_dh}, {p->dx, p->ld_dx}});
+    const bool whole = r.ok && !r.shift;
+    // short rows; element by element the ring overtakes on many rows (bf16,
+    // 30810x207: 22.0 us here, 19.0 there; 255x207: 3.7, 5.5)
+    const bool many = p->M > (int64_t)32 * d.sms;
+    if (whole ? p->N <= kBwdShortVectors * V : p->N <= (many ? kBwdShortElements / 2 : kBwdShortElements)) {
+        P.short_rows = true;
+        P.vec = whole;
+        const int64_t passes = (p->M + add_bwd_short_rows(P.vec, p->N, V) - 1) / add_bwd_short_rows(P.vec, p->N, V);
+        if (p->G > passes) p->G = static_cast<int>(passes);
+        return P;
+    }
     const int G = phase_grid(p->M, r.phases, d, p->G);
     if (!r.ok || G < 1) return P;
     const int stat_rows = static_cast<int>((p->M + G - 1) / G);
@@ -920,7 +946,8 @@ int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *
         p.err = d.err;
         p.wait_ns = o.wait_ns;
         const AddBwdPlan P = o.kernel == GBN_KERNEL_AUTO ? add_bwd_plan(dtype, d, &p) : AddBwdPlan();
-        st = cuda_status(P.ok ? launch_rms_add_bwd_ring(dtype, P.nv, P.shift, p, P.smem, stream)
+        st = cuda_status(P.short_rows ? launch_rms_add_bwd_short(dtype, P.vec, p, stream)
+                         : P.ok       ? launch_rms_add_bwd_ring(dtype, P.nv, P.shift, p, P.smem, stream)
                               : launch_rms_add_bwd_plain(dtype, p, stream));
         if (st != GBN_OK) return st;
         // the partial rows of the CTAs that ran

@@ -30,4 +30,17 @@ cudaError_t launch_rms_add_bwd_ring(int dtype, int nv, bool shift, const AddBwdP
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_rms_add_bwd_short_f32(bool, const AddBwdParams &, cudaStream_t);
+cudaError_t launch_rms_add_bwd_short_f16(bool, const AddBwdParams &, cudaStream_t);
+cudaError_t launch_rms_add_bwd_short_bf16(bool, const AddBwdParams &, cudaStream_t);
+
+cudaError_t launch_rms_add_bwd_short(int dtype, bool vec, const AddBwdParams &p, cudaStream_t s) {
+    switch (dtype) {
+        case 0: return launch_rms_add_bwd_short_f32(vec, p, s);
+        case 1: return launch_rms_add_bwd_short_f16(vec, p, s);
+        case 2: return launch_rms_add_bwd_short_bf16(vec, p, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace gbn

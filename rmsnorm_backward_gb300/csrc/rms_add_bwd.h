@@ -55,6 +55,16 @@ __host__ __device__ constexpr bool add_bwd_gamma_smem(size_t es, int nv) { retur
 
 constexpr int kAddBwdThreads = 512;
 
+// the longest rows of the short-row kernel, in 16-byte vectors and in
+// elements, and the rows that a CTA of it takes at once
+constexpr int kBwdShortVectors = 64, kBwdShortElements = 256;
+inline int add_bwd_short_rows(bool vec, int N, int V) {
+    if (!vec) return N <= 128 ? 32 : 16;
+    const int nvec = N / V;
+    return nvec <= 8 ? 128 : nvec <= 16 ? 64 : nvec <= 32 ? 32 : 16;
+}
+// vec: rows of whole 16-byte vectors, else element by element
+cudaError_t launch_rms_add_bwd_short(int dtype, bool vec, const AddBwdParams &p, cudaStream_t s);
 cudaError_t launch_rms_add_bwd_plain(int dtype, const AddBwdParams &p, cudaStream_t s);
 // nv: vectors a thread owns (1 to 4; float32 also 6 and 8); shift: some row does
 // not start or end on 16 bytes

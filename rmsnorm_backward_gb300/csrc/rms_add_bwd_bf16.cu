@@ -12,4 +12,8 @@ cudaError_t launch_rms_add_bwd_ring_bf16(int nv, bool shift, const AddBwdParams 
     return rms_add_bwd_ring_dispatch<__nv_bfloat16>(nv, shift, p, smem, s);
 }
 
+cudaError_t launch_rms_add_bwd_short_bf16(bool vec, const AddBwdParams &p, cudaStream_t s) {
+    return rms_add_bwd_short_dispatch<__nv_bfloat16>(vec, p, s);
+}
+
 }  // namespace gbn

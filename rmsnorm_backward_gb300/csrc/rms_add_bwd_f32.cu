@@ -12,4 +12,8 @@ cudaError_t launch_rms_add_bwd_ring_f32(int nv, bool shift, const AddBwdParams &
     return rms_add_bwd_ring_dispatch<float>(nv, shift, p, smem, s);
 }
 
+cudaError_t launch_rms_add_bwd_short_f32(bool vec, const AddBwdParams &p, cudaStream_t s) {
+    return rms_add_bwd_short_dispatch<float>(vec, p, s);
+}
+
 }  // namespace gbn

@@ -370,4 +370,125 @@ cudaError_t rms_add_bwd_plain_dispatch(const AddBwdParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Short rows: L lanes of a warp to a row, 32 / L rows at once in a warp; loads
+// go straight to registers, the CTA's warps hide them.  C: elements to an
+// access, a 16-byte vector's or one (rows that do not lie on 16 bytes); a lane
+// owns NV accesses, L apart, and their dgamma sums.  At the end a warp's rows
+// meet in shuffles and the warps in shared memory, in warp order.
+// ---------------------------------------------------------------------------
+template <typename T, int L, int NV, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) rms_add_bwd_short_kernel(const AddBwdParams p) {
+    using Tr = Traits<T>;
+    constexpr int C = VEC ? Tr::kVec : 1;
+    constexpr int E = NV * C;
+    constexpr int WIDTH = L * E;  // columns
+    __shared__ float sums[THREADS / 32][WIDTH];
+    const int N = p.N, lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5;
+    const float inv_n = 1.0f / static_cast<float>(N);
+    griddep_launch_dependents();
+    float gam[E], acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (lane + (e / C) * L) * C + e % C;
+        gam[e] = c < N ? Tr::load1(static_cast<const T *>(p.gamma) + c) : 0.f;
+        acc[e] = 0.f;
+    }
+    const int64_t rows = (int64_t)gridDim.x * (THREADS / L);
+    // rounds are the whole warp's: its lanes meet in shuffles
+    for (int64_t r0 = (blockIdx.x * (int64_t)THREADS + threadIdx.x) / 32 * (32 / L); r0 < p.M; r0 += rows) {
+        const int64_t row = r0 + (threadIdx.x & 31) / L;
+        const bool live = row < p.M;
+        const T *hp = static_cast<const T *>(p.h) + row * p.ld_h;
+        const T *dp = static_cast<const T *>(p.dy) + row * p.ld_dy;
+        const T *ep = static_cast<const T *>(p.dh) + row * p.ld_dh;
+        const float rs = live ? p.rstd[row] : 0.f;
+        float h[E], d[E], o[E];
+        if constexpr (VEC) {
+            uint4 h4[NV], d4[NV], e4[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * L) * C;
+                const bool in = live && c < N;
+                h4[j] = in ? *reinterpret_cast<const uint4 *>(hp + c) : make_uint4(0, 0, 0, 0);
+                d4[j] = in ? *reinterpret_cast<const uint4 *>(dp + c) : make_uint4(0, 0, 0, 0);
+                e4[j] = in ? *reinterpret_cast<const uint4 *>(ep + c) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                Tr::unpack(h4[j], h + j * C);
+                Tr::unpack(d4[j], d + j * C);
+                Tr::unpack(e4[j], o + j * C);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = lane + j * L;
+                const bool in = live && c < N;
+                h[j] = in ? Tr::load1(hp + c) : 0.f;
+                d[j] = in ? Tr::load1(dp + c) : 0.f;
+                o[j] = in ? Tr::load1(ep + c) : 0.f;
+            }
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum = fmaf(d[e] * gam[e], h[e], sum);
+#pragma unroll
+        for (int s = L / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        // D = dy*rstd, a = -rstd^2 * mean(dyhat*xhat): dgamma += D*h, dx = D*gamma + (h*a + dh)
+        const float a = -rs * rs * (sum * rs * inv_n);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float D = d[e] * rs;
+            acc[e] = fmaf(D, h[e], acc[e]);
+            o[e] = fmaf(D, gam[e], fmaf(h[e], a, o[e]));
+        }
+        T *dx = static_cast<T *>(p.dx) + row * p.ld_dx;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (lane + j * L) * C;
+            if (live && c < N) {
+                if constexpr (VEC)
+                    *reinterpret_cast<uint4 *>(dx + c) = Tr::pack(o + j * C);
+                else
+                    Tr::store1(dx + c, o[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+#pragma unroll
+        for (int s = 16; s >= L; s >>= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], s);
+        if ((threadIdx.x & 31) < L) sums[warp][(lane + (e / C) * L) * C + e % C] = acc[e];
+    }
+    __syncthreads();
+    float *part = p.part + (size_t)blockIdx.x * p.ldp;
+    for (int c = threadIdx.x; c < N; c += THREADS) {
+        float t = sums[0][c];
+        for (int w = 1; w < THREADS / 32; ++w) t += sums[w][c];
+        part[c] = t;
+    }
+}
+
+template <typename T, int L, int NV, bool VEC, int THREADS>
+cudaError_t rms_add_bwd_short_launch(const AddBwdParams &p, cudaStream_t s) {
+    rms_add_bwd_short_kernel<T, L, NV, VEC, THREADS><<<p.G, THREADS, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+// the rows at once are add_bwd_short_rows()'s
+template <typename T>
+cudaError_t rms_add_bwd_short_dispatch(bool vec, const AddBwdParams &p, cudaStream_t s) {
+    if (vec) {
+        const int nvec = p.N / Traits<T>::kVec;
+        if (nvec <= 8) return rms_add_bwd_short_launch<T, 8, 1, true, 1024>(p, s);
+        if (nvec <= 16) return rms_add_bwd_short_launch<T, 16, 1, true, 1024>(p, s);
+        if (nvec <= 32) return rms_add_bwd_short_launch<T, 32, 1, true, 1024>(p, s);
+        return rms_add_bwd_short_launch<T, 32, 2, true, 512>(p, s);
+    }
+    if (p.N <= 64) return rms_add_bwd_short_launch<T, 32, 2, false, 1024>(p, s);
+    if (p.N <= 128) return rms_add_bwd_short_launch<T, 32, 4, false, 1024>(p, s);
+    return rms_add_bwd_short_launch<T, 32, 8, false, 512>(p, s);
+}
+
 }  // namespace gbn

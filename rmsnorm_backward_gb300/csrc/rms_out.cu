@@ -16,15 +16,28 @@ cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParam
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_rms_out_ring_f32(int, bool, const OutParams &, size_t, cudaStream_t);
-cudaError_t launch_rms_out_ring_f16(int, bool, const OutParams &, size_t, cudaStream_t);
-cudaError_t launch_rms_out_ring_bf16(int, bool, const OutParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_out_ring_f32(int, int, const OutParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_out_ring_f16(int, int, const OutParams &, size_t, cudaStream_t);
+cudaError_t launch_rms_out_ring_bf16(int, int, const OutParams &, size_t, cudaStream_t);
 
-cudaError_t launch_rms_out_ring(int dtype, int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
+cudaError_t launch_rms_out_ring(int dtype, int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (dtype) {
-        case 0: return launch_rms_out_ring_f32(nv, full, p, smem, s);
-        case 1: return launch_rms_out_ring_f16(nv, full, p, smem, s);
-        case 2: return launch_rms_out_ring_bf16(nv, full, p, smem, s);
+        case 0: return launch_rms_out_ring_f32(nv, lie, p, smem, s);
+        case 1: return launch_rms_out_ring_f16(nv, lie, p, smem, s);
+        case 2: return launch_rms_out_ring_bf16(nv, lie, p, smem, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_rms_out_short_f32(bool, const OutParams &, int, cudaStream_t);
+cudaError_t launch_rms_out_short_f16(bool, const OutParams &, int, cudaStream_t);
+cudaError_t launch_rms_out_short_bf16(bool, const OutParams &, int, cudaStream_t);
+
+cudaError_t launch_rms_out_short(int dtype, bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    switch (dtype) {
+        case 0: return launch_rms_out_short_f32(vec, p, sms, s);
+        case 1: return launch_rms_out_short_f16(vec, p, sms, s);
+        case 2: return launch_rms_out_short_bf16(vec, p, sms, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -37,7 +37,6 @@ struct OutParams {
     int nvec;            // 16-byte vectors that a row touches, at most
     int shift0, shift_step;  // row_shift's (row_phase.h)
     int late;            // a stage is refilled after its row's stores, not before
-    int across;          // some row does not start or end on 16 bytes
     int codes_aligned;   // a vector's codes can be stored at once
     int *err;
 };
@@ -60,9 +59,16 @@ __host__ __device__ inline OutLayout out_layout(int slots, int stages, int strea
 
 constexpr int kOutThreads = 512;
 
-// nv: vectors a thread owns (1, 2, 4; float32 also 8); full: every row is
-// nv * tpr whole vectors
-cudaError_t launch_rms_out_ring(int dtype, int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s);
+// the longest rows of the short-row kernel, in 16-byte vectors and in elements
+constexpr int kShortVectors = 64, kShortElements = 512;
+
+// how rows lie to 16-byte boundaries (rms_out_kernels.cuh)
+enum RowLie : int { kLieFull = 0, kLieWhole = 1, kLieAcross = 2 };
+
+// nv: vectors a thread owns (1 to 4; float32 also 6 and 8)
+cudaError_t launch_rms_out_ring(int dtype, int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s);
+// vec: rows of whole 16-byte vectors (their codes on V), else element by element
+cudaError_t launch_rms_out_short(int dtype, bool vec, const OutParams &p, int sms, cudaStream_t s);
 cudaError_t launch_rms_out_plain(int dtype, int kind, bool group, const OutParams &p, int sms, cudaStream_t s);
 
 }  // namespace gbn

@@ -7,8 +7,12 @@ cudaError_t launch_rms_out_plain_bf16(int kind, bool group, const OutParams &p, 
     return rms_out_plain_dispatch<__nv_bfloat16>(kind, group, p, sms, s);
 }
 
-cudaError_t launch_rms_out_ring_bf16(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
-    return rms_out_ring_dispatch<__nv_bfloat16>(nv, full, p, smem, s);
+cudaError_t launch_rms_out_ring_bf16(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    return rms_out_ring_dispatch<__nv_bfloat16>(nv, lie, p, smem, s);
+}
+
+cudaError_t launch_rms_out_short_bf16(bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    return rms_out_short_dispatch<__nv_bfloat16>(vec, p, sms, s);
 }
 
 }  // namespace gbn

@@ -7,8 +7,12 @@ cudaError_t launch_rms_out_plain_f16(int kind, bool group, const OutParams &p, i
     return rms_out_plain_dispatch<__half>(kind, group, p, sms, s);
 }
 
-cudaError_t launch_rms_out_ring_f16(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
-    return rms_out_ring_dispatch<__half>(nv, full, p, smem, s);
+cudaError_t launch_rms_out_ring_f16(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    return rms_out_ring_dispatch<__half>(nv, lie, p, smem, s);
+}
+
+cudaError_t launch_rms_out_short_f16(bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    return rms_out_short_dispatch<__half>(vec, p, sms, s);
 }
 
 }  // namespace gbn

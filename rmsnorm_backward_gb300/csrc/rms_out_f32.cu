@@ -7,8 +7,12 @@ cudaError_t launch_rms_out_plain_f32(int kind, bool group, const OutParams &p, i
     return rms_out_plain_dispatch<float>(kind, group, p, sms, s);
 }
 
-cudaError_t launch_rms_out_ring_f32(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
-    return rms_out_ring_dispatch<float>(nv, full, p, smem, s);
+cudaError_t launch_rms_out_ring_f32(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    return rms_out_ring_dispatch<float>(nv, lie, p, smem, s);
+}
+
+cudaError_t launch_rms_out_short_f32(bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    return rms_out_short_dispatch<float>(vec, p, sms, s);
 }
 
 }  // namespace gbn

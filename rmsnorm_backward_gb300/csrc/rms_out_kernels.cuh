@@ -219,15 +219,20 @@ cudaError_t rms_out_plain_dispatch(int kind, bool group, const OutParams &p, int
 // refilled; then the outputs are written from registers: x and residual are
 // read once, h is written once and read by nobody.
 //
-// FULL: rows that start and end on 16 bytes (their codes on V) and are as many
-// vectors as the slot's threads own.  Otherwise a thread may own fewer, and rows may lie
-// across 16-byte boundaries, all tensors' alike (the host checks that): such a
-// row is copied with the up to 14 bytes before and after it that share its
-// first and last 16 bytes (never beyond the tensor's first and last element:
-// those two ends are copied element by element); only the vectors that lie
-// wholly in the row are the threads', and the elements before and after them
-// go to the lanes of the slot's last warp, one each.  The maxima of groups
-// then meet in shared memory, as their borders run through vectors.
+// How the rows lie (RowLie):
+//  * kLieFull: they start and end on 16 bytes (their codes on V) and are as
+//    many vectors as the slot's threads own;
+//  * kLieWhole: a thread may own fewer;
+//  * kLieAcross: rows may lie across 16-byte boundaries, all tensors' alike
+//    (the host checks that): such a row is copied with the up to 14 bytes
+//    before and after it that share its first and last 16 bytes (never beyond
+//    the tensor's first and last element: those two ends are copied element by
+//    element); only the vectors that lie wholly in the row are the threads',
+//    and the elements before and after them go to the lanes of the slot's last
+//    warp, one each.  The maxima of groups then meet in shared memory, as
+//    their borders run through vectors.
+// The first two leave out what the third needs: 16384x4096 bf16 to e4m3, without
+// the residual, 67 us as kLieAcross alone, 52 as kLieFull.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ float round_to(float f) {
@@ -277,12 +282,13 @@ __device__ __forceinline__ void store_codes(uint8_t *at, uint2 code, int lane, i
     if (lane < 2 * V && (lane < V) == (e < V - m)) at[(lane < V ? 0 : (live - 1) * V) + e] = static_cast<uint8_t>(end >> (8 * e));
 }
 
-template <typename T, int KIND, bool GROUP, int NV, bool FULL>
+template <typename T, int KIND, bool GROUP, int NV, int LIE>
 __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutParams p) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     constexpr int E = NV * V;
     constexpr bool QUANT = KIND != kOutSame;
+    constexpr bool FULL = LIE == kLieFull, ACROSS = LIE == kLieAcross;
     constexpr bool GRAW = sizeof(T) == 2 && NV > 2;  // gamma kept in the storage type
     using Out = typename std::conditional<QUANT, uint8_t, T>::type;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const int N = p.N, S = p.stages;
     const uint32_t rowb = static_cast<uint32_t>(p.nvec) * 16;
     const int groups = (N + kQuantGroup - 1) / kQuantGroup;
-    const bool meet = GROUP && !FULL && p.across;  // group maxima through shared memory
+    constexpr bool meet = GROUP && ACROSS;  // group maxima through shared memory
     const OutLayout L = out_layout(slots, S, streams, p.nvec, meet ? groups : 0);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar);
     float *reds = reinterpret_cast<float *>(smem + L.red);
@@ -308,12 +314,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const int ns = slot < slots && row < p.M ? static_cast<int>((p.M - row + row_step - 1) / row_step) : 0;
     // the row starts s elements into its first vector; vectors [vb, ve) lie
     // wholly in it
-    const int s = FULL ? 0 : row_shift(blockIdx.x, p.shift0, p.shift_step, V);
-    const int nvec = FULL ? p.nvec : (s + N + V - 1) / V;
+    const int s = !ACROSS ? 0 : row_shift(blockIdx.x, p.shift0, p.shift_step, V);
+    const int nvec = !ACROSS ? p.nvec : (s + N + V - 1) / V;
     const int vb = s > 0 ? 1 : 0, ve = (s + N) / V;
     // the lane's element beside them, as a place in the staged row: s <= ce < s + N, or -1
     int ce = -1;
-    if (!FULL && warp == W - 1) {
+    if (ACROSS && warp == W - 1) {
         if (lane < V)
             ce = s > 0 && lane >= s && lane < s + N ? lane : -1;
         else if (lane < 2 * V && ve >= vb)
@@ -341,8 +347,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
         uint32_t from = 0, to = bytes;
         unsigned char *dst = ring + (pst * streams + lane) * rowb;
-        const int64_t r = FULL ? 1 : row0 + issued * row_step;
-        if (!FULL && (r == 0 || r == p.M - 1)) {
+        const int64_t r = !ACROSS ? 1 : row0 + issued * row_step;
+        if (ACROSS && (r == 0 || r == p.M - 1)) {
             // the tensors' first and last rows: nothing outside them is read
             if (lane < streams) {
                 if (src < base) from = 16;
@@ -472,7 +478,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 }
             }
         }
-        if (!FULL && ce >= 0) {
+        if (ACROSS && ce >= 0) {
             he = Tr::load1(reinterpret_cast<const T *>(sx) + ce);
             if (res) {
                 he = round_to<T>(he + Tr::load1(reinterpret_cast<const T *>(sx + rowb) + ce));
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     st_global_cs_v4(out + v * V, Tr::pack(o));
                 }
             }
-            if (!FULL && ce >= 0) Tr::store1(out + ce, ge * (he * rs));
+            if (ACROSS && ce >= 0) Tr::store1(out + ce, ge * (he * rs));
         } else {
             float qf = 0.f;
             if constexpr (!GROUP) {
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 float *t = held + j * V;
                 uint2 code = make_uint2(0, 0);
                 float m = most;
-                if (meet) {
+                if constexpr (meet) {
                     // the vector's columns in one group or two
                     const int c0 = v < ve ? v * V - s : 0, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
                     m = __uint_as_float(gm[g]);
@@ -616,9 +622,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     code.x = quant4_finite<KIND>(t);
                     if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
                 }
-                store_codes<V>(out + v0 * V, code, lane, FULL || ve - v0 > 32 ? 32 : ve - v0, FULL || p.codes_aligned);
+                store_codes<V>(out + v0 * V, code, lane, FULL || ve - v0 > 32 ? 32 : ve - v0, !ACROSS || p.codes_aligned);
             }
-            if (!FULL && ce >= 0) {
+            if (ACROSS && ce >= 0) {
                 if constexpr (GROUP) {
                     const float a = __uint_as_float(gm[(ce - s) / kQuantGroup]);
                     out[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
@@ -646,48 +652,249 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     }
 }
 
-template <typename T, int KIND, bool GROUP, int NV, bool FULL>
+template <typename T, int KIND, bool GROUP, int NV, int LIE>
 cudaError_t rms_out_ring_launch(const OutParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, GROUP, NV, FULL>, done);
+    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, GROUP, NV, LIE>, done);
     if (e != cudaSuccess) return e;
-    rms_out_ring_kernel<T, KIND, GROUP, NV, FULL><<<p.G, kOutThreads, smem, s>>>(p);
+    rms_out_ring_kernel<T, KIND, GROUP, NV, LIE><<<p.G, kOutThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
+template <typename T, int KIND, bool GROUP, int NV>
+cudaError_t rms_out_ring_lie(int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    if constexpr ((NV & (NV - 1)) == 0) {
+        if (lie == kLieFull) return rms_out_ring_launch<T, KIND, GROUP, NV, kLieFull>(p, smem, s);
+    }
+    return lie == kLieAcross ? rms_out_ring_launch<T, KIND, GROUP, NV, kLieAcross>(p, smem, s)
+                             : rms_out_ring_launch<T, KIND, GROUP, NV, kLieWhole>(p, smem, s);
+}
+
 template <typename T, int KIND, bool GROUP>
-cudaError_t rms_out_ring_nv(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
+cudaError_t rms_out_ring_nv(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (nv) {
-#define GBN_CASE(n)                                                               \
-    case n:                                                                       \
-        return full ? rms_out_ring_launch<T, KIND, GROUP, n, true>(p, smem, s)    \
-                    : rms_out_ring_launch<T, KIND, GROUP, n, false>(p, smem, s)
-        GBN_CASE(1);
-        GBN_CASE(2);
-        GBN_CASE(4);
-#undef GBN_CASE
-        case 3: return rms_out_ring_launch<T, KIND, GROUP, 3, false>(p, smem, s);
-        case 6:
-            if constexpr (sizeof(T) == 4) return rms_out_ring_launch<T, KIND, GROUP, 6, false>(p, smem, s);
-            break;
-        case 8:
-            if constexpr (sizeof(T) == 4)
-                return full ? rms_out_ring_launch<T, KIND, GROUP, 8, true>(p, smem, s)
-                            : rms_out_ring_launch<T, KIND, GROUP, 8, false>(p, smem, s);
+        case 1: return rms_out_ring_lie<T, KIND, GROUP, 1>(lie, p, smem, s);
+        case 2: return rms_out_ring_lie<T, KIND, GROUP, 2>(lie, p, smem, s);
+        case 3: return rms_out_ring_lie<T, KIND, GROUP, 3>(lie, p, smem, s);
+        case 4: return rms_out_ring_lie<T, KIND, GROUP, 4>(lie, p, smem, s);
+    }
+    if constexpr (sizeof(T) == 4) {
+        if (nv == 6) return rms_out_ring_lie<T, KIND, GROUP, 6>(lie, p, smem, s);
+        if (nv == 8) return rms_out_ring_lie<T, KIND, GROUP, 8>(lie, p, smem, s);
     }
     return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t rms_out_ring_dispatch(int nv, bool full, const OutParams &p, size_t smem, cudaStream_t s) {
+cudaError_t rms_out_ring_dispatch(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (p.kind) {
-        case kOutSame: return rms_out_ring_nv<T, kOutSame, false>(nv, full, p, smem, s);
+        case kOutSame: return rms_out_ring_nv<T, kOutSame, false>(nv, lie, p, smem, s);
         case kOutE4M3:
-            return p.group ? rms_out_ring_nv<T, kOutE4M3, true>(nv, full, p, smem, s)
-                           : rms_out_ring_nv<T, kOutE4M3, false>(nv, full, p, smem, s);
+            return p.group ? rms_out_ring_nv<T, kOutE4M3, true>(nv, lie, p, smem, s)
+                           : rms_out_ring_nv<T, kOutE4M3, false>(nv, lie, p, smem, s);
         case kOutInt8:
-            return p.group ? rms_out_ring_nv<T, kOutInt8, true>(nv, full, p, smem, s)
-                           : rms_out_ring_nv<T, kOutInt8, false>(nv, full, p, smem, s);
+            return p.group ? rms_out_ring_nv<T, kOutInt8, true>(nv, lie, p, smem, s)
+                           : rms_out_ring_nv<T, kOutInt8, false>(nv, lie, p, smem, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// Short rows: L lanes of a warp to a row, so a warp has 32 / L rows at once and
+// a row costs no exchange beyond the warp; loads go straight to registers, many
+// warps on an SM hide them.  C: elements to an access, a 16-byte vector's or
+// one (rows that do not lie on 16 bytes); a lane owns NV accesses, L apart.
+// ---------------------------------------------------------------------------
+constexpr int kShortThreads = 256;
+
+template <typename T, int KIND, bool GROUP, int L, int NV, bool VEC>
+__global__ void __launch_bounds__(kShortThreads) rms_out_short_kernel(const OutParams p) {
+    using Tr = Traits<T>;
+    constexpr int C = VEC ? Tr::kVec : 1;
+    constexpr int E = NV * C;
+    constexpr bool QUANT = KIND != kOutSame;
+    static_assert(!GROUP || L == 32, "groups of a row that the whole warp holds");
+    // groups of 128 columns: of GL lanes each in every access (vectors), or
+    // of 128 / L accesses of all lanes (elements)
+    constexpr int GL = VEC ? kQuantGroup / C : 32, NG = !GROUP ? 1 : VEC ? NV : NV * L / kQuantGroup;
+    const int N = p.N, lane = threadIdx.x & (L - 1);
+    const bool res = QUANT ? p.res != nullptr : true;
+    const float inv_n = 1.0f / static_cast<float>(N);
+    float gam[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int c = (lane + (e / C) * L) * C + e % C;
+        gam[e] = c < N ? Tr::load1(static_cast<const T *>(p.gamma) + c) : 0.f;
+    }
+    const int64_t rows = (int64_t)gridDim.x * (kShortThreads / L);
+    // rounds are the whole warp's: its lanes meet in shuffles
+    for (int64_t r0 = (blockIdx.x * (int64_t)kShortThreads + threadIdx.x) / 32 * (32 / L); r0 < p.M; r0 += rows) {
+        const int64_t row = r0 + (threadIdx.x & 31) / L;
+        const bool live = row < p.M;
+        const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
+        const T *r = res ? static_cast<const T *>(p.res) + row * p.ld_res : nullptr;
+        T *h = res ? static_cast<T *>(p.h) + row * p.ld_h : nullptr;
+        float f[E];
+        if constexpr (VEC) {
+            uint4 x4[NV], r4[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * L) * C;
+                const bool in = live && c < N;
+                x4[j] = in ? *reinterpret_cast<const uint4 *>(x + c) : make_uint4(0, 0, 0, 0);
+                if (res) r4[j] = in ? *reinterpret_cast<const uint4 *>(r + c) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * L) * C;
+                float a[C];
+                Tr::unpack(x4[j], a);
+                if (res) {
+                    float b[C];
+                    Tr::unpack(r4[j], b);
+#pragma unroll
+                    for (int e = 0; e < C; ++e) a[e] += b[e];
+                    const uint4 h4 = Tr::pack(a);
+                    if (live && c < N) *reinterpret_cast<uint4 *>(h + c) = h4;
+                    Tr::unpack(h4, a);
+                }
+#pragma unroll
+                for (int e = 0; e < C; ++e) f[j * C + e] = a[e];
+            }
+        } else {
+            float b[E];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = lane + j * L;
+                f[j] = live && c < N ? Tr::load1(x + c) : 0.f;
+                if (res) b[j] = live && c < N ? Tr::load1(r + c) : 0.f;
+            }
+            if (res) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = lane + j * L;
+                    f[j] = round_to<T>(f[j] + b[j]);
+                    if (live && c < N) Tr::store1(h + c, f[j]);
+                }
+            }
+        }
+        float sum = 0.f, most[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) most[g] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            sum = fmaf(f[e], f[e], sum);
+            if constexpr (QUANT) {
+                f[e] *= gam[e];
+                most[e / (E / NG)] = max_nan(most[e / (E / NG)], fabsf(f[e]));
+            }
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (QUANT && (!GROUP || o < GL)) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) most[g] = max_nan(most[g], __shfl_xor_sync(0xffffffffu, most[g], o));
+            }
+        }
+        const float rs = __frsqrt_rn(fmaf(sum, inv_n, p.eps));
+        if (!live) continue;
+        if (lane == 0) {
+            p.rstd[row] = rs;
+            if constexpr (QUANT && !GROUP) p.scale[row] = quant_scale<KIND>(rs, most[0]);
+        }
+        if constexpr (GROUP) {
+            const int groups = (N + kQuantGroup - 1) / kQuantGroup;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int at = VEC ? lane / GL + g * (32 / GL) : g;
+                if (lane % GL == 0 && at < groups) p.scale[row * groups + at] = quant_scale<KIND>(rs, most[g]);
+            }
+        }
+        if constexpr (!QUANT) {
+            T *y = static_cast<T *>(p.out) + row * p.ld_out;
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = gam[e] * (f[e] * rs);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * L) * C;
+                if (c < N) {
+                    if constexpr (VEC)
+                        *reinterpret_cast<uint4 *>(y + c) = Tr::pack(f + j * C);
+                    else
+                        Tr::store1(y + c, f[j]);
+                }
+            }
+        } else {
+            uint8_t *q = static_cast<uint8_t *>(p.out) + row * p.ld_out;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float qf = quant_factor<KIND>(most[g]), raise = quant_tiny(most[g]) ? kRaise : 1.f;
+#pragma unroll
+                for (int e = 0; e < E / NG; ++e) f[g * (E / NG) + e] = (f[g * (E / NG) + e] * raise) * qf;
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (lane + j * L) * C;
+                if (c < N) {
+                    if constexpr (VEC) {
+                        const float *t = f + j * C;
+                        uint2 code;
+                        code.x = quant4<KIND>(t[0], t[1], t[2], t[3]);
+                        if constexpr (C == 8) {
+                            code.y = quant4<KIND>(t[4], t[5], t[6], t[7]);
+                            *reinterpret_cast<uint2 *>(q + c) = code;
+                        } else {
+                            *reinterpret_cast<uint32_t *>(q + c) = code.x;
+                        }
+                    } else {
+                        q[c] = quant1<KIND>(f[j]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int KIND, bool GROUP, int L, int NV, bool VEC>
+cudaError_t rms_out_short_launch(const OutParams &p, int sms, cudaStream_t s) {
+    const int64_t want = (p.M + kShortThreads / L - 1) / (kShortThreads / L), most = (int64_t)sms * 8;
+    rms_out_short_kernel<T, KIND, GROUP, L, NV, VEC>
+        <<<static_cast<int>(want < most ? want : most), kShortThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+// vec: rows of whole 16-byte vectors, codes that can be stored V at a time.
+// Groups of columns: rows longer than one (a shorter row is one group).
+template <typename T, int KIND>
+cudaError_t rms_out_short_kind(bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    const int nvec = p.N / Traits<T>::kVec;
+    if constexpr (KIND != kOutSame) {
+        if (p.group) {
+            if (vec && nvec <= 32) return rms_out_short_launch<T, KIND, true, 32, 1, true>(p, sms, s);
+            if (vec) return rms_out_short_launch<T, KIND, true, 32, 2, true>(p, sms, s);
+            if (p.N <= 256) return rms_out_short_launch<T, KIND, true, 32, 8, false>(p, sms, s);
+            return rms_out_short_launch<T, KIND, true, 32, 16, false>(p, sms, s);
+        }
+    }
+    if (vec) {
+        if (nvec <= 8) return rms_out_short_launch<T, KIND, false, 8, 1, true>(p, sms, s);
+        if (nvec <= 16) return rms_out_short_launch<T, KIND, false, 16, 1, true>(p, sms, s);
+        if (nvec <= 32) return rms_out_short_launch<T, KIND, false, 32, 1, true>(p, sms, s);
+        return rms_out_short_launch<T, KIND, false, 32, 2, true>(p, sms, s);
+    }
+    if (p.N <= 64) return rms_out_short_launch<T, KIND, false, 32, 2, false>(p, sms, s);
+    if (p.N <= 128) return rms_out_short_launch<T, KIND, false, 32, 4, false>(p, sms, s);
+    if (p.N <= 256) return rms_out_short_launch<T, KIND, false, 32, 8, false>(p, sms, s);
+    return rms_out_short_launch<T, KIND, false, 32, 16, false>(p, sms, s);
+}
+
+template <typename T>
+cudaError_t rms_out_short_dispatch(bool vec, const OutParams &p, int sms, cudaStream_t s) {
+    switch (p.kind) {
+        case kOutSame: return rms_out_short_kind<T, kOutSame>(vec, p, sms, s);
+        case kOutE4M3: return rms_out_short_kind<T, kOutE4M3>(vec, p, sms, s);
+        case kOutInt8: return rms_out_short_kind<T, kOutInt8>(vec, p, sms, s);
     }
     return cudaErrorInvalidValue;
 }
