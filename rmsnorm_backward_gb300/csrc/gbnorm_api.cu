@@ -658,6 +658,9 @@ struct RowSpan {
     int64_t ld, row;
 };
 
+// whether offsets of M rows of stride ld stay within 64 bits, in bytes
+bool in_reach(int64_t M, int64_t ld) { return M <= 1 || ld <= (int64_t(1) << 59) / M; }
+
 bool same_rows(const RowSpan &a, const RowSpan &b) { return a.p == b.p && a.ld == b.ld && a.row == b.row; }
 
 // Whether the rows of a and of b have no byte in common.  Rows of one stride
@@ -717,9 +720,9 @@ RowPhases row_phases(int es, int64_t M, int N, const RowBase (&t)[K]) {
     return r;
 }
 
-// CTAs for rows of `phases` phases: a multiple of it, or one for each row
-// (0: neither).
-int phase_grid(int64_t M, int phases, const DevInfo &d, int most) {
+// CTAs (at most `most`) for rows of `phases` phases: a multiple of it, or one
+// for each row.
+int phase_grid(int64_t M, int phases, int most) {
     int G = M < most ? static_cast<int>(M) : most;
     if (G == M) return G;
     return G / phases * phases;
@@ -800,7 +803,7 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
         P.vec = whole;
         return P;
     }
-    const int G = phase_grid(p->M, r.phases, d, d.sms);
+    const int G = phase_grid(p->M, r.phases, d.sms);
     if (!r.ok || G < 1 || p->M / G >= (1 << 30)) return P;
     const int groups = !whole && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
     // without a residual to read, the row's work next to its bytes is more, and
@@ -845,6 +848,7 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     if (!ld_out) ld_out = N;
     if (!ld_h) ld_h = N;
     if (ld_x < N || ld_res < N || ld_out < N || ld_h < N) return GBN_EINVAL;
+    if (!in_reach(M, ld_x) || !in_reach(M, ld_res) || !in_reach(M, ld_out) || !in_reach(M, ld_h)) return GBN_EINVAL;
     if (M == 0) return GBN_OK;
     if (!x || !gamma || !out || !rstd || (has_res && (!res || !h)) || (kind != kOutSame && !scale)) return GBN_EINVAL;
     const int64_t es = elem_bytes(dtype), eo = kind == kOutSame ? es : 1;
@@ -900,7 +904,7 @@ AddBwdPlan add_bwd_plan(int dtype, const DevInfo &d, AddBwdParams *p) {
         if (p->G > passes) p->G = static_cast<int>(passes);
         return P;
     }
-    const int G = phase_grid(p->M, r.phases, d, p->G);
+    const int G = phase_grid(p->M, r.phases, p->G);
     if (!r.ok || G < 1) return P;
     const int stat_rows = static_cast<int>((p->M + G - 1) / G);
     const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 48, 100, 150, {1, 2, 3, 4, 6, 8}, [&](int nv, int slots) {
@@ -925,6 +929,7 @@ int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *
     if (st == GBN_OK) st = resolve_options(opt, N, dtype, &o);
     if (st != GBN_OK) return st;
     if (!ld_dh) ld_dh = N;
+    if (!in_reach(M, ld_dh) || !in_reach(M, o.ld_x) || !in_reach(M, o.ld_dy) || !in_reach(M, o.ld_out)) return GBN_EINVAL;
     if (ld_dh < N || o.reduce_mode != GBN_REDUCE_PARTIALS || o.kernel == GBN_KERNEL_SLOT || !dgamma) return GBN_EINVAL;
     if (M > 0) {
         if (!dy || !dh || !h || !gamma || !rstd || !dx || !workspace) return GBN_EINVAL;
@@ -1021,7 +1026,7 @@ size_t gbn_grad_workspace_bytes(void) {
 
 int gbn_grad_norm(const gbn_tensor *tensors, int64_t count, float *norm, void *workspace, size_t workspace_bytes,
                   cudaStream_t stream) {
-    if (!valid_tensors(tensors, count) || !norm || !workspace) return GBN_EINVAL;
+    if (!valid_tensors(tensors, count) || !norm || !workspace || !element_aligned(4, norm)) return GBN_EINVAL;
     DevInfo d;
     const int st = device_info(&d);
     if (st != GBN_OK) return st;
@@ -1031,7 +1036,7 @@ int gbn_grad_norm(const gbn_tensor *tensors, int64_t count, float *norm, void *w
 
 int gbn_grad_clip(const gbn_tensor *tensors, const gbn_tensor *out, int64_t count, float max_norm, float eps,
                   float *norm, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-    if (!valid_tensors(tensors, count) || !norm || !workspace) return GBN_EINVAL;
+    if (!valid_tensors(tensors, count) || !norm || !workspace || !element_aligned(4, norm)) return GBN_EINVAL;
     if (!(max_norm >= 0.f) || !(eps >= 0.f)) return GBN_EINVAL;
     if (out) {
         if (!valid_tensors(out, count)) return GBN_EINVAL;

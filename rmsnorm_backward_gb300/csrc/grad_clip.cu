@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_clip_kernel
     const float norm = norm_of(t.partial, t.total, sm);
     if (blockIdx.x == 0 && threadIdx.x == 0 && !t.add) *t.norm = norm;
     const float c = t.max_norm / (norm + t.eps);
-    const float coef = c >= 1.f ? 1.f : c;  // NaN stays NaN
+    const float coef = c >= 1.f || norm == 0.f ? 1.f : c;  // a norm that is NaN stays NaN
     uint32_t c0, k;
     cta_range(t.chunks, c0, k);
     if (c0 >= k) return;

@@ -130,6 +130,8 @@ def test_zeros_and_values_that_are_not_finite():
     t = [torch.ones(100, device="cuda")]
     gbn.grad_clip(t, float("inf"))
     assert (t[0] == 1).all()
+    gbn.grad_clip(z, 0.0, eps=0.0)  # 0 / 0
+    assert all((x == 0).all() for x in z)
 
 
 def test_the_same_bits_from_run_to_run():

@@ -59,6 +59,14 @@ def test_forward_arguments(lib, call):
         assert call(lib, ld=tuple(7 if j == i else 0 for j in range(strides))) == EINVAL
 
 
+@pytest.mark.parametrize("call", [add_fwd, add_q8, q8])
+def test_addresses_and_reach(lib, call):
+    for k in ("x", "g", "rstd"):
+        assert call(lib, **{k: at(0x100001)}) == EINVAL  # between two elements
+    far = (1 << 60, 0) if call is q8 else (1 << 60, 0, 0, 0)
+    assert call(lib, ld=far) == EINVAL  # rows beyond 64 bits
+
+
 @pytest.mark.parametrize("call", [add_q8, q8])
 def test_quantization_arguments(lib, call):
     assert call(lib, q_dtype=BF16) == EDTYPE
@@ -107,6 +115,9 @@ def test_backward_arguments(lib):
     assert add_bwd(lib, dx=at(X.value + 2)) == EINVAL
     assert add_bwd(lib, dx=at(R.value + 16)) == EINVAL
     assert add_bwd(lib, dx=H, ld_out=9) == EINVAL
+    assert add_bwd(lib, dy=at(0x100001)) == EINVAL
+    assert add_bwd(lib, dg=at(0x700002)) == EINVAL
+    assert add_bwd(lib, ld_dh=1 << 60) == EINVAL
 
 
 def table(*entries):
@@ -126,6 +137,7 @@ def test_gradient_arguments(lib):
         assert call(None, 2) == EINVAL
         assert call(good, 2, norm=None) == EINVAL
         assert call(good, 2, ws=None) == EINVAL
+        assert call(good, 2, norm=at(0x102)) == EINVAL
         assert call(table((0x1002, 4, 0)), 1) == EINVAL      # not aligned to its element
         assert call(table((0x1001, 4, 1)), 1) == EINVAL
         assert call(table((0, 4, 1)), 1) == EINVAL           # no address

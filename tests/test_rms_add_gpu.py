@@ -488,3 +488,81 @@ def test_refusals():
     with pytest.raises(gbn.GbnError) as e:
         gbn.rms_add_bwd(x, x.clone(), x.clone(), g, r, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 4
+
+
+def test_backward_wait_that_runs_out():
+    """A wait limit far below a copy's latency: the kernel reports error 1 and returns, and the next call is right."""
+    import ctypes
+
+    M, N = 2000, 4096
+    t = inputs(M, N, "bf16", seed=14)
+    d = {k: v.cuda() for k, v in t.items()}
+    _, h, rstd = gbn.rms_add_fwd(d["x"], d["residual"], d["gamma"], EPS)
+    dx, dg = torch.empty_like(h), torch.empty(N, device="cuda")
+    ws = torch.empty(gbn.bwd_workspace_bytes(M, N, h.dtype, False), dtype=torch.uint8, device="cuda")
+    assert gbn.device_error() == 0
+    opt = gbn.GbnOptions(0, 0, 0, 0, 0, 0, 0, 0, 1)
+    s = torch.cuda.current_stream().cuda_stream
+    assert gbn.lib().rms_add_bwd(d["dy"].data_ptr(), d["dh"].data_ptr(), h.data_ptr(), d["gamma"].data_ptr(),
+                                 rstd.data_ptr(), dx.data_ptr(), dg.data_ptr(), M, N, 2, ws.data_ptr(), ws.numel(), 0,
+                                 ctypes.byref(opt), s) == 0
+    assert gbn.device_error(clear=True) == 1
+    gbn.rms_add_bwd(d["dy"], d["dh"], h, d["gamma"], rstd, dx=dx, dgamma=dg, workspace=ws)
+    assert gbn.device_error() == 0
+    check_backward(t, h.cpu(), rstd.cpu(), dx, dg)
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch
+import rmsnorm_backward_gb300 as gbn
+x = torch.randn(64, 1536, device="cuda", dtype=torch.bfloat16)
+r, dy, dh = (torch.randn_like(x) for _ in range(3))
+g = torch.ones(1536, device="cuda", dtype=torch.bfloat16)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y, h, rstd = gbn.rms_add_fwd(x, r, g, 1e-6)
+    q, scale, _ = gbn.rms_fwd_q8(h, g, 1e-6)
+    dx, dg = gbn.rms_add_bwd(dy, dh, h, g, rstd)
+    norm = gbn.grad_clip([dg], 0.5)
+graph.replay()
+torch.cuda.synchronize()
+y2, h2, rstd2 = gbn.rms_add_fwd(x, r, g, 1e-6)
+dx2, dg2 = gbn.rms_add_bwd(dy, dh, h2, g, rstd2)
+assert torch.equal(y, y2) and torch.equal(dx, dx2)
+assert torch.equal(norm, gbn.grad_clip([dg2], 0.5)) and torch.equal(dg, dg2)
+assert gbn.device_error() == 0
+print("captured")
+"""
+
+
+def test_first_call_in_a_capture():
+    """A process whose first calls are captured ones."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_streams_at_once():
+    """The same inputs on two streams, each call with buffers of its own."""
+    M, N = 4000, 4096
+    t = inputs(M, N, "bf16", seed=15)
+    d = {k: v.cuda() for k, v in t.items()}
+    _, h, rstd = gbn.rms_add_fwd(d["x"], d["residual"], d["gamma"], EPS)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = []
+    for _ in range(3):
+        for s in streams:
+            out.append(gbn.rms_add_fwd(d["x"], d["residual"], d["gamma"], EPS, stream=s)
+                       + gbn.rms_add_bwd(d["dy"], d["dh"], h, d["gamma"], rstd, stream=s))
+    torch.cuda.synchronize()
+    for o in out:
+        assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
+    check_forward(t, *out[0][:3])
+    check_backward(t, h.cpu(), rstd.cpu(), *out[0][3:])
