@@ -83,12 +83,44 @@ __device__ __forceinline__ uint32_t quant4_finite(const float *t) {
         return quant4<KIND>(t[0], t[1], t[2], t[3]);
     } else {
         constexpr float kRound = 12582912.f;
-        const float2 k2 = make_float2(kRound, kRound);
-        const float2 a = pair_add(make_float2(t[0], t[1]), k2), b = pair_add(make_float2(t[2], t[3]), k2);
-        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(t[0], kRound)),
+                                        __float_as_uint(__fadd_rn(t[1], kRound)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(t[2], kRound)),
+                                        __float_as_uint(__fadd_rn(t[3], kRound)), 0x0040);
         return __byte_perm(lo, hi, 0x5410);
     }
+}
+// Whether a maximum has an ordinary factor: not zero, tiny, infinite or NaN.
+__device__ __forceinline__ bool quant_plain(float a) { return a >= kTiny && a < __int_as_float(0x7f800000); }
+// the codes of four values whose maximum a has none
+template <int KIND>
+__device__ __noinline__ uint32_t quant4_odd(float v0, float v1, float v2, float v3, float a) {
+    const float raise = quant_tiny(a) ? kRaise : 1.f, f = quant_factor<KIND>(a);
+    return quant4<KIND>((v0 * raise) * f, (v1 * raise) * f, (v2 * raise) * f, (v3 * raise) * f);
+}
+// the codes of a lane's V values (code.x the first four's) by the factor of
+// their maximum a
+template <int KIND, int V>
+__device__ __forceinline__ uint2 quant_vector(float *t, float factor, float a) {
+    uint2 code = make_uint2(0, 0);
+    if (quant_plain(a)) {
+        // int8: the product is rounded before the addition that rounds it to
+        // an integer.  As pairs the two came out as one fused operation, which
+        // rounds ties the other way.
+        const float2 f2 = make_float2(factor, factor);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 w = KIND == kOutInt8 ? make_float2(__fmul_rn(t[2 * i], factor), __fmul_rn(t[2 * i + 1], factor))
+                                              : pair_mul(pair_at(t, i), f2);
+            t[2 * i] = w.x, t[2 * i + 1] = w.y;
+        }
+        code.x = quant4_finite<KIND>(t);
+        if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
+    } else {
+        code.x = quant4_odd<KIND>(t[0], t[1], t[2], t[3], a);
+        if constexpr (V == 8) code.y = quant4_odd<KIND>(t[4], t[5], t[6], t[7], a);
+    }
+    return code;
 }
 template <int KIND>
 __device__ __forceinline__ uint8_t quant1(float a) {
@@ -553,11 +585,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 most = __uint_as_float(bits);
                 qf = quant_factor<KIND>(most);
                 if (ts == 0) p.scale[row] = quant_scale<KIND>(rs, most);
-                if (quant_tiny(most)) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) held[e] *= kRaise;
-                    he *= kRaise;
-                }
             }
             float *scale = p.scale + (GROUP ? row * groups : 0);
             if (meet) {
@@ -568,59 +595,54 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     scale[i] = quant_scale<KIND>(rs, __uint_as_float(gm[i]));
                 }
             }
+            if constexpr (GROUP && !ACROSS) {
+                // The maximum of a group from its lanes (16 of a 16-bit type,
+                // 32 of float32); lane j of them divides for their vector j
+                // and writes its scale: one division a row, not one a vector.
+                constexpr int GL = kQuantGroup / V;
+                float mine = 0.f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    uint32_t b = __float_as_uint(vmost[j]);
+                    if constexpr (GL == 32) {
+                        b = __reduce_max_sync(0xffffffffu, b);
+                    } else {
+#pragma unroll
+                        for (int o = GL / 2; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+                    }
+                    vmost[j] = __uint_as_float(b);
+                    if ((lane & (GL - 1)) == j) mine = vmost[j];
+                }
+                qf = quant_factor<KIND>(mine);
+                const int at = (ts - lane) + (lane & (GL - 1)) * tpr + (lane & ~(GL - 1));  // its vector
+                if ((lane & (GL - 1)) < NV && at < ve) scale[at / GL] = quant_scale<KIND>(rs, mine);
+            }
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int v0 = vb + (ts - lane) + j * tpr, v = v0 + lane;
                 if (!FULL && v0 >= ve) break;  // the whole warp
                 float *t = held + j * V;
                 uint2 code = make_uint2(0, 0);
-                float m = most;
                 if constexpr (meet) {
                     // the vector's columns in one group or two
                     const int c0 = v < ve ? v * V - s : 0, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
-                    m = __uint_as_float(gm[g]);
-                    const float f0 = quant_factor<KIND>(m), r0 = quant_tiny(m) ? kRaise : 1.f;
+                    const float m = __uint_as_float(gm[g]), f0 = quant_factor<KIND>(m);
+                    const float r0 = quant_tiny(m) ? kRaise : 1.f;
                     float f1 = f0, r1 = r0;
                     if (split < V) {
                         const float m1 = __uint_as_float(gm[g + 1]);
                         f1 = quant_factor<KIND>(m1), r1 = quant_tiny(m1) ? kRaise : 1.f;
-                        m = max_nan(m, m1);
                     }
 #pragma unroll
                     for (int e = 0; e < V; ++e) t[e] = (t[e] * (e < split ? r0 : r1)) * (e < split ? f0 : f1);
-                } else {
-                    if constexpr (GROUP) {
-                        // 128 columns: 16 lanes of a 16-bit type, 32 of float32
-                        uint32_t b = __float_as_uint(vmost[j]);
-                        if constexpr (V == 4) {
-                            b = __reduce_max_sync(0xffffffffu, b);
-                        } else {
-#pragma unroll
-                            for (int o = kQuantGroup / V / 2; o > 0; o >>= 1)
-                                b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-                        }
-                        m = __uint_as_float(b);
-                        qf = quant_factor<KIND>(m);
-                        if ((lane & (kQuantGroup / V - 1)) == 0 && (FULL || v < ve))
-                            scale[v * V / kQuantGroup] = quant_scale<KIND>(rs, m);
-                        if (quant_tiny(m)) {
-#pragma unroll
-                            for (int e = 0; e < V; ++e) t[e] *= kRaise;
-                        }
-                    }
-                    const float2 f2 = make_float2(qf, qf);
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i) {
-                        const float2 w = pair_mul(pair_at(t, i), f2);
-                        t[2 * i] = w.x, t[2 * i + 1] = w.y;
-                    }
-                }
-                if (KIND == kOutInt8 && !(m < __int_as_float(0x7f800000))) {
                     code.x = quant4<KIND>(t[0], t[1], t[2], t[3]);
                     if constexpr (V == 8) code.y = quant4<KIND>(t[4], t[5], t[6], t[7]);
+                } else if constexpr (GROUP) {
+                    constexpr int GL = kQuantGroup / V;
+                    const float f = __shfl_sync(0xffffffffu, qf, (lane & ~(GL - 1)) + j);
+                    code = quant_vector<KIND, V>(t, f, vmost[j]);
                 } else {
-                    code.x = quant4_finite<KIND>(t);
-                    if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
+                    code = quant_vector<KIND, V>(t, qf, most);
                 }
                 store_codes<V>(out + v0 * V, code, lane, FULL || ve - v0 > 32 ? 32 : ve - v0, !ACROSS || p.codes_aligned);
             }
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     const float a = __uint_as_float(gm[(ce - s) / kQuantGroup]);
                     out[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
                 } else {
-                    out[ce] = quant1<KIND>(he * qf);
+                    out[ce] = quant1<KIND>((he * (quant_tiny(most) ? kRaise : 1.f)) * qf);
                 }
             }
         }

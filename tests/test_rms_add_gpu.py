@@ -566,3 +566,22 @@ def test_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
     check_forward(t, *out[0][:3])
     check_backward(t, h.cpu(), rstd.cpu(), *out[0][3:])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_codes_at_ties(dtype, group):
+    """Values half way between two codes in float32, on rows of every kernel: many rows of few-bit values, whose products
+    with the factor often are such."""
+    g = torch.Generator().manual_seed(16)
+    for N in (64, 496, 640, 1024, 4096, 4808, 8192, 1001, 4099):
+        x = (torch.randint(-128, 129, (120, N), generator=g).float() / 64).to(DT[dtype])
+        x[:, 0] = 127.0 / 64
+        gamma = torch.ones(N, dtype=DT[dtype])
+        for q_dtype in gbn.Q_DTYPE_CODES:
+            q, scale, rstd = gbn.rms_fwd_q8(x.cuda(), gamma.cuda(), EPS, q_dtype=q_dtype, group=group)
+            code, _ = codes_and_scale(x, gamma, rstd.cpu(), q_dtype, group)
+            assert torch.equal(q.cpu().view(torch.uint8), code.view(torch.uint8)), (N, q_dtype)
+            q, scale, _, rstd = gbn.rms_add_fwd_q8(x.cuda(), torch.zeros_like(x).cuda(), gamma.cuda(), EPS,
+                                                   q_dtype=q_dtype, group=group)
+            assert torch.equal(q.cpu().view(torch.uint8), code.view(torch.uint8)), (N, q_dtype)
