@@ -819,11 +819,11 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec;
     p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
     if (r.shift0 != 0 || r.step != 0) p->codes_aligned = 0;
-    // wide rows: two stages already are more in flight than HBM likes beside
-    // the writes, so a stage is refilled after its row's stores (8192x16384
-    // bf16 to e4m3 by 128 columns: 157.6 us before them, 142.9 after; on
-    // narrower rows it costs 5%)
-    p->late = p->kind != kOutSame && s.slots == 1 && r.nvec * 16 * streams > 60 * 1024;
+    // Wide rows: two stages already are more in flight than HBM likes beside
+    // the writes, so a stage is refilled only once the next one has landed
+    // (8192x16384 bf16: 171.1 us without that, 160.5 with; to e4m3 by 128
+    // columns 164.5, 145.5; 16384x4096: 82.0, 91.1).
+    p->late = s.slots == 1 && r.nvec * 16 * streams > 60 * 1024;
     // neighbouring rows to a CTA's slots, where every CTA has a few rounds of
     // them; otherwise rows G apart, which all have one shift
     const bool near = !r.shift && p->M >= (int64_t)4 * G * s.slots;

@@ -36,7 +36,7 @@ struct OutParams {
     int stages;          // ring stages per slot
     int nvec;            // 16-byte vectors that a row touches, at most
     int shift0, shift_step;  // row_shift's (row_phase.h)
-    int late;            // a stage is refilled after its row's stores, not before
+    int late;            // a stage is refilled once the next one has landed, not before
     int codes_aligned;   // a vector's codes can be stored at once
     int *err;
 };

@@ -445,6 +445,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     for (; k < ns; ++k, row += row_step) {
         const bool timed_out = !mbar_wait_bounded(&bar[pos.stage], pos.parity);
         if (timed_out) record_error(p.err, kErrWaitFull);
+        if (p.late && issuer && k > 0 && issued < ns) {  // the row before is in registers, this one landed
+            fence_proxy_async();
+            issue();
+        }
         const unsigned char *sx = ring + pos.stage * streams * rowb;
         uint32_t *gm = gmax + buf * groups;
         T *h = static_cast<T *>(p.h) + (res ? row * p.ld_h - s : 0);
@@ -654,10 +658,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     out[ce] = quant1<KIND>((he * (quant_tiny(most) ? kRaise : 1.f)) * qf);
                 }
             }
-        }
-        if (p.late && issuer && issued < ns) {
-            fence_proxy_async();
-            issue();
         }
         buf = buf == 2 ? 0 : buf + 1;
         pos.next(S);
