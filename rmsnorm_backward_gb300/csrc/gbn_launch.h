@@ -153,6 +153,23 @@ cudaError_t ensure_smem_optin(K kernel, std::atomic<uint64_t> &done) {
     return e;
 }
 
+// Launches `kernel` as a programmatic dependent of what is before it on the
+// stream: it may start, up to its griddep_wait(), while that still runs.
+template <typename K, typename P>
+cudaError_t launch_dependent(K kernel, int grid, int threads, size_t smem, cudaStream_t s, const P &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // activation backward dx = dy * f'(preact) over n contiguous elements
 enum : int { kActSilu = 0, kActGelu = 1 };
 struct ActParams {

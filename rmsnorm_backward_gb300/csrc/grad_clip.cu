@@ -345,20 +345,6 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_clip_kernel
     }
 }
 
-template <typename K, typename P>
-cudaError_t launch_pdl(K kernel, int grid, cudaStream_t s, const P &p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kGradThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 // One pass over the list: tables of up to CAP tensors, a launch for each.
 template <int CAP>
 cudaError_t run_list(const gbn_tensor *g, const gbn_tensor *out, int64_t count, bool clip, int grid, float max_norm,
@@ -386,8 +372,8 @@ cudaError_t run_list(const gbn_tensor *g, const gbn_tensor *out, int64_t count, 
         }
         t.chunks = static_cast<uint32_t>(chunks);
         t.add = first ? 0 : 1;
-        const cudaError_t r = clip ? launch_pdl(grad_clip_kernel<CAP>, grid, s, t)
-                                   : launch_pdl(grad_norm_kernel<CAP>, grid, s, t);
+        const cudaError_t r = clip ? launch_dependent(grad_clip_kernel<CAP>, grid, kGradThreads, 0, s, t)
+                                   : launch_dependent(grad_norm_kernel<CAP>, grid, kGradThreads, 0, s, t);
         if (r != cudaSuccess) return r;
         first = false;
     } while (i < count);

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
     for (int i = tid; i < slots * 2 * kRedStride; i += kAddBwdThreads) reds[i] = 0.f;
     if (tid < slots) flags[tid] = 0;
     __syncthreads();
+    griddep_wait();  // whatever is before this kernel on the stream
 
     // lane t < 3 of the issuing warp copies tensor t's rows
     unsigned char *ring = smem + (size_t)slot * S * 3 * rowb;
@@ -380,8 +381,7 @@ cudaError_t rms_add_bwd_ring_launch(const AddBwdParams &p, size_t smem, cudaStre
     static std::atomic<uint64_t> done{0};
     cudaError_t e = ensure_smem_optin(rms_add_bwd_ring_kernel<T, NV, SHIFT>, done);
     if (e != cudaSuccess) return e;
-    rms_add_bwd_ring_kernel<T, NV, SHIFT><<<p.G, kAddBwdThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(rms_add_bwd_ring_kernel<T, NV, SHIFT>, p.G, kAddBwdThreads, smem, s, p);
 }
 
 template <typename T>
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1) rms_add_bwd_short_kernel(const Add
     __shared__ float sums[THREADS / 32][WIDTH];
     const int N = p.N, lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5;
     const float inv_n = 1.0f / static_cast<float>(N);
+    griddep_wait();  // whatever is before this kernel on the stream
     griddep_launch_dependents();
     float gam[E], acc[E];
 #pragma unroll
@@ -515,8 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1) rms_add_bwd_short_kernel(const Add
 
 template <typename T, int L, int NV, bool VEC, int THREADS>
 cudaError_t rms_add_bwd_short_launch(const AddBwdParams &p, cudaStream_t s) {
-    rms_add_bwd_short_kernel<T, L, NV, VEC, THREADS><<<p.G, THREADS, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(rms_add_bwd_short_kernel<T, L, NV, VEC, THREADS>, p.G, THREADS, 0, s, p);
 }
 
 // the rows at once are add_bwd_short_rows()'s

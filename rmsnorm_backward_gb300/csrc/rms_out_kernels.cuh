@@ -367,6 +367,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         for (int i = tid; i < slots * 3 * groups; i += kOutThreads) reinterpret_cast<uint32_t *>(smem + L.gmax)[i] = 0;
     if (tid < slots) flags[tid] = 0;
     __syncthreads();
+    griddep_wait();  // whatever is before this kernel on the stream
+    griddep_launch_dependents();
 
     // lane t < streams of the issuing warp copies tensor t's rows
     unsigned char *ring = smem + (size_t)slot * S * streams * rowb;
@@ -679,8 +681,7 @@ cudaError_t rms_out_ring_launch(const OutParams &p, size_t smem, cudaStream_t s)
     static std::atomic<uint64_t> done{0};
     cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, GROUP, NV, LIE>, done);
     if (e != cudaSuccess) return e;
-    rms_out_ring_kernel<T, KIND, GROUP, NV, LIE><<<p.G, kOutThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(rms_out_ring_kernel<T, KIND, GROUP, NV, LIE>, p.G, kOutThreads, smem, s, p);
 }
 
 template <typename T, int KIND, bool GROUP, int NV>
@@ -742,6 +743,8 @@ __global__ void __launch_bounds__(kShortThreads) rms_out_short_kernel(const OutP
     const int N = p.N, lane = threadIdx.x & (L - 1);
     const bool res = QUANT ? p.res != nullptr : true;
     const float inv_n = 1.0f / static_cast<float>(N);
+    griddep_wait();  // whatever is before this kernel on the stream
+    griddep_launch_dependents();
     float gam[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -881,9 +884,8 @@ __global__ void __launch_bounds__(kShortThreads) rms_out_short_kernel(const OutP
 template <typename T, int KIND, bool GROUP, int L, int NV, bool VEC>
 cudaError_t rms_out_short_launch(const OutParams &p, int sms, cudaStream_t s) {
     const int64_t want = (p.M + kShortThreads / L - 1) / (kShortThreads / L), most = (int64_t)sms * 8;
-    rms_out_short_kernel<T, KIND, GROUP, L, NV, VEC>
-        <<<static_cast<int>(want < most ? want : most), kShortThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(rms_out_short_kernel<T, KIND, GROUP, L, NV, VEC>,
+                            static_cast<int>(want < most ? want : most), kShortThreads, 0, s, p);
 }
 
 // vec: rows of whole 16-byte vectors, codes that can be stored V at a time.
