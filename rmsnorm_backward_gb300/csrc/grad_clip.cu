@@ -21,6 +21,12 @@
 //  * clip: every CTA forms coef from the partial sums itself (no kernel in
 //    between), then walks its chunks backwards: what the first pass read
 //    last is still in L2.  In place with coef = 1 there is nothing to do.
+// Both are bound by HBM: 480 MB of float32 in 76.8 us (norm only, 6.25 TB/s,
+// 93% of the measured copy rate), 671 MB of bf16 clipped into other tensors in
+// 316 us (two reads and a write, 6.4 TB/s), 126 MB in 61 us (the second read
+// mostly from L2).  Four CTAs of 256 threads an SM with 32 KiB chunks: six, or
+// 16 KiB, took 3 to 8% longer; evict-first hints on all but the last chunks of
+// the first pass won 2% of a large clip and lost 4% of a norm.
 #include "gbn_device.cuh"
 #include "grad_clip.h"
 
