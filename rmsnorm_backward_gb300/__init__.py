@@ -442,10 +442,12 @@ def gelu_bwd(dy: torch.Tensor, preact: torch.Tensor, *, dx: Optional[torch.Tenso
 # RMSNorm with the residual's addition and / or an 8-bit output, its backward
 # ---------------------------------------------------------------------------
 _ROW_KERNELS = {"auto": 0, "plain": 2}
-# the current stream's handle without a Stream object, where torch has it: a
-# call on a few rows costs the host more than the GPU, and the object alone
-# 1.9 of 13.5 us
+# A call on a few rows costs the host more than the GPU, so these functions
+# ask each tensor for as little as the checks need: dtypes are compared by
+# identity, devices by index, and the current stream's handle comes without a
+# Stream object where torch has it (that alone was 1.9 of 13.5 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_f32 = torch.float32
 
 
 def _enqueue(fn: str, device, stream, args, owned=()) -> None:
@@ -454,10 +456,10 @@ def _enqueue(fn: str, device, stream, args, owned=()) -> None:
     than the one they were allocated on, their memory stays theirs until that
     stream is done with it."""
     call = getattr(_lib or lib(), fn)
-    if stream is not None or _raw_stream is None:
-        handle = _stream(device, stream)
-    else:
+    if stream is None and _raw_stream is not None:
         handle = _raw_stream(device.index)
+    else:
+        handle = _stream(device, stream)
     if torch.cuda.current_device() == device.index:
         status = call(*args, handle)
     else:
@@ -474,9 +476,14 @@ def _enqueue(fn: str, device, stream, args, owned=()) -> None:
 
 def _rows_like(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """Row stride of t, which must have this shape, dtype and device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device.index:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
     return shape[-1] if t.is_contiguous() else _rows_ld(t, name)[2]
+
+
+def _vec_like(t: torch.Tensor, name: str, n: int, dtype, device) -> None:
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device.index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
 
 
 def _new(shape, dtype, device, owned) -> torch.Tensor:
@@ -497,12 +504,12 @@ def rms_add_fwd(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, ep
     M, N, ld_x = _rows_ld(x, "x")
     shape, dtype, device, owned = x.shape, x.dtype, x.device, []
     ld_r = _rows_like(residual, "residual", shape, dtype, device)
-    _vec(gamma, "gamma", N, dtype, device)
+    _vec_like(gamma, "gamma", N, dtype, device)
     y = _new(shape, dtype, device, owned) if y is None else y
     h = _new(shape, dtype, device, owned) if h is None else h
-    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
+    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
     ld_y, ld_h = _rows_like(y, "y", shape, dtype, device), _rows_like(h, "h", shape, dtype, device)
-    _vec(rstd, "rstd", M, torch.float32, device)
+    _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_add_fwd", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), y.data_ptr(), h.data_ptr(), rstd.data_ptr(),
               eps, M, N, _code(x), ld_x, ld_r, ld_y, ld_h, _ROW_KERNELS[kernel]), owned)
@@ -519,8 +526,8 @@ def _q8_args(shape, device, q_dtype, group, q, scale, owned):
     q = _new(shape, q_dtype, device, owned) if q is None else q
     ld_q = _rows_like(q, "q", shape, q_dtype, device)
     scales = shape[:-1] + ((shape[-1] + QUANT_GROUP - 1) // QUANT_GROUP,) if group else shape[:-1]
-    scale = _new(scales, torch.float32, device, owned) if scale is None else scale
-    if scale.shape != scales or scale.dtype != torch.float32 or scale.device != device or not scale.is_contiguous():
+    scale = _new(scales, _f32, device, owned) if scale is None else scale
+    if scale.shape != scales or scale.dtype is not _f32 or scale.get_device() != device.index or not scale.is_contiguous():
         raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(scales)} on {device}")
     return q, ld_q, scale, Q_DTYPE_CODES[q_dtype]
 
@@ -536,10 +543,10 @@ def rms_fwd_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, q_dtype=torc
     q_dtype.  kernel: "auto" or "plain"."""
     M, N, ld_x = _rows_ld(x, "x")
     device, owned = x.device, []
-    _vec(gamma, "gamma", N, x.dtype, device)
+    _vec_like(gamma, "gamma", N, x.dtype, device)
     q, ld_q, scale, q_code = _q8_args(x.shape, device, q_dtype, group, q, scale, owned)
-    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
-    _vec(rstd, "rstd", M, torch.float32, device)
+    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
+    _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_fwd_q8", device, stream,
              (x.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), eps, M, N, _code(x),
               q_code, group, ld_x, ld_q, _ROW_KERNELS[kernel]), owned)
@@ -556,12 +563,12 @@ def rms_add_fwd_q8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
     M, N, ld_x = _rows_ld(x, "x")
     shape, dtype, device, owned = x.shape, x.dtype, x.device, []
     ld_r = _rows_like(residual, "residual", shape, dtype, device)
-    _vec(gamma, "gamma", N, dtype, device)
+    _vec_like(gamma, "gamma", N, dtype, device)
     q, ld_q, scale, q_code = _q8_args(shape, device, q_dtype, group, q, scale, owned)
     h = _new(shape, dtype, device, owned) if h is None else h
-    rstd = _new(M, torch.float32, device, owned) if rstd is None else rstd
+    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
     ld_h = _rows_like(h, "h", shape, dtype, device)
-    _vec(rstd, "rstd", M, torch.float32, device)
+    _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_add_fwd_q8", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), h.data_ptr(),
               rstd.data_ptr(), eps, M, N, _code(x), q_code, group, ld_x, ld_r, ld_q, ld_h, _ROW_KERNELS[kernel]),
@@ -581,24 +588,24 @@ def rms_add_bwd(dy: torch.Tensor, dh: torch.Tensor, h: torch.Tensor, gamma: torc
     "plain"."""
     M, N, ld_h = _rows_ld(h, "h")
     shape, dtype, device, owned = h.shape, h.dtype, h.device, []
-    if grad_dtype != torch.float32 and grad_dtype != dtype:
+    if grad_dtype is not _f32 and grad_dtype is not dtype:
         raise ValueError("grad_dtype must be float32 or h's dtype")
     ld_dy, ld_dh = _rows_like(dy, "dy", shape, dtype, device), _rows_like(dh, "dh", shape, dtype, device)
-    _vec(gamma, "gamma", N, dtype, device)
-    _vec(rstd, "rstd", M, torch.float32, device)
+    _vec_like(gamma, "gamma", N, dtype, device)
+    _vec_like(rstd, "rstd", M, _f32, device)
     dx = _new(shape, dtype, device, owned) if dx is None else dx
     ld_dx = _rows_like(dx, "dx", shape, dtype, device)
     if dgamma is None:
         dgamma = _grads(None, "dgamma", N, grad_dtype, device, accumulate)
         owned.append(dgamma)
     else:
-        _vec(dgamma, "dgamma", N, grad_dtype, device)
+        _vec_like(dgamma, "dgamma", N, grad_dtype, device)
     if workspace is None:
         workspace = _new(max(bwd_workspace_bytes(M, N, dtype, False, device), 1), torch.uint8, device, owned)
-    elif workspace.device != device or not workspace.is_contiguous():
+    elif workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on h's device")
     opt = None
-    if accumulate or kernel != "auto" or grad_dtype != torch.float32 or not ld_h == ld_dy == ld_dx == N:
+    if accumulate or kernel != "auto" or grad_dtype is not _f32 or not ld_h == ld_dy == ld_dx == N:
         opt = ctypes.byref(GbnOptions(ld_h, ld_dy, ld_dx, 1 if accumulate else 0, DTYPE_CODES[grad_dtype], 0,
                                       _ROW_KERNELS[kernel], 0, 0))
     _enqueue("rms_add_bwd", device, stream,
@@ -693,11 +700,11 @@ def _grad_args(grads, norm, workspace, owned):
         norm = torch.empty((), dtype=torch.float32, device=device)
         owned.append(norm)
     else:
-        _vec(norm, "norm", 1, torch.float32, device)
+        _vec_like(norm, "norm", 1, _f32, device)
     if workspace is None:
         workspace = torch.empty(grad_workspace_bytes(device), dtype=torch.uint8, device=device)
         owned.append(workspace)
-    elif workspace.device != device or not workspace.is_contiguous():
+    elif workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the gradients' device")
     return grads, norm, workspace, device
 
