@@ -105,13 +105,12 @@ __device__ __forceinline__ uint2 quant_vector(float *t, float factor, float a) {
     uint2 code = make_uint2(0, 0);
     if (quant_plain(a)) {
         // int8: the product is rounded before the addition that rounds it to
-        // an integer.  As pairs the two came out as one fused operation, which
-        // rounds ties the other way.
+        // an integer.  With both as pairs they came out as one fused operation,
+        // which rounds ties the other way; so the additions are scalar.
         const float2 f2 = make_float2(factor, factor);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const float2 w = KIND == kOutInt8 ? make_float2(__fmul_rn(t[2 * i], factor), __fmul_rn(t[2 * i + 1], factor))
-                                              : pair_mul(pair_at(t, i), f2);
+            const float2 w = pair_mul(pair_at(t, i), f2);
             t[2 * i] = w.x, t[2 * i + 1] = w.y;
         }
         code.x = quant4_finite<KIND>(t);
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     constexpr int E = NV * V;
     constexpr bool QUANT = KIND != kOutSame;
     constexpr bool FULL = LIE == kLieFull, ACROSS = LIE == kLieAcross;
-    constexpr bool GRAW = sizeof(T) == 2 && NV > 2;  // gamma kept in the storage type
+    constexpr bool GRAW = sizeof(T) == 2 && NV > 3;  // gamma kept in the storage type
     using Out = typename std::conditional<QUANT, uint8_t, T>::type;
     extern __shared__ __align__(128) unsigned char smem[];
 
@@ -551,10 +550,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             sum = 0.f;
             for (int w = 0; w < W; w += 4) {
                 const float4 t = *reinterpret_cast<const float4 *>(b + w);
-                sum += t.x;
-                sum += t.y;
-                sum += t.z;
-                sum += t.w;
+                sum += (t.x + t.y) + (t.z + t.w);
                 if constexpr (QUANT && !GROUP) {
                     const uint4 m = *reinterpret_cast<const uint4 *>(b + kRedStride + w);
                     bits = max(max(max(bits, m.x), max(m.y, m.z)), m.w);
