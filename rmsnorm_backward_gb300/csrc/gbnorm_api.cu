@@ -755,6 +755,10 @@ SlotPlan slot_plan(int V, int whole, int64_t stage, int kb, int kb_alone, std::i
         if (slots > fit) slots = static_cast<int>(fit);
         if (slots < 1 || (busy && slots * w < 14)) continue;
         busy = slots * w, P.tpr = 32 * w, P.slots = slots, P.nv = n;
+        // the fewest that the same warps hold the row with (27711x2202 bf16 to
+        // int8, 3 warps: 4 91 us, 3 75)
+        for (int m : counts)
+            if (m < P.nv && m * P.tpr >= whole) P.nv = m;
     }
     if (!busy) return P;
     // Stages: about kb KB of copies in flight, kb_alone where one slot has the
@@ -805,20 +809,23 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     }
     const int G = phase_grid(p->M, r.phases, d.sms);
     if (!r.ok || G < 1 || p->M / G >= (1 << 30)) return P;
-    const int groups = !whole && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
+    const bool shift = !whole && !p->res;
+    const int groups = !whole && p->res && p->group ? (p->N + kQuantGroup - 1) / kQuantGroup : 0;
     // without a residual to read, the row's work next to its bytes is more, and
     // more vectors a thread spread what a row costs besides them (e4m3,
-    // 16384x4096 bf16: 2 52 us, 4 40 us)
-    const std::initializer_list<int> two = {1, 2, 3, 4, 6, 8}, four = {1, 4, 2, 3, 6, 8};
-    const SlotPlan s = slot_plan(V, p->N / V, (int64_t)r.nvec * 16 * streams, p->res ? 64 : 96,
-                                 p->kind == kOutSame ? 64 : 128, p->res ? two : four, [&](int, int slots) {
+    // 16384x4096 bf16: 2 52 us, 4 40 us); where the maxima of groups meet in
+    // shared memory three are between (16384x2050 bf16: 2 82 us, 3 70; 701
+    // columns of float32 42 and 35)
+    const std::initializer_list<int> two = {1, 2, 3, 4, 6, 8}, four = {1, 4, 2, 3, 6, 8}, three = {1, 3, 2, 4, 6, 8};
+    const SlotPlan s = slot_plan(V, (shift || groups ? p->N + V - 1 : p->N) / V, (int64_t)r.nvec * 16 * streams, p->res ? 64 : 96,
+                                 p->kind == kOutSame ? 64 : 128, groups ? three : p->res ? two : four, [&](int, int slots) {
         return static_cast<int64_t>(d.smem_optin) - static_cast<int64_t>(out_layout(slots, 16, 0, 0, groups).total);
     });
     if (!s.ok) return P;
     p->G = G;
     p->shift0 = r.shift0, p->shift_step = r.step, p->nvec = r.nvec;
     p->tpr = s.tpr, p->slots = s.slots, p->stages = s.stages;
-    if (r.shift0 != 0 || r.step != 0) p->codes_aligned = 0;
+    if (!shift && (r.shift0 != 0 || r.step != 0)) p->codes_aligned = 0;
     // Wide rows: two stages already are more in flight than HBM likes beside
     // the writes, so a stage is refilled only once the next one has landed
     // (8192x16384 bf16: 171.1 us without that, 160.5 with; to e4m3 by 128
@@ -830,7 +837,7 @@ OutPlan out_plan(int dtype, const DevInfo &d, OutParams *p) {
     p->cta_step = near ? s.slots : 1;
     p->slot_step = near ? 1 : G;
     P.ok = true, P.nv = s.nv;
-    P.lie = !whole ? kLieAcross : r.nvec == s.nv * s.tpr && (s.nv & (s.nv - 1)) == 0 ? kLieFull : kLieWhole;
+    P.lie = shift ? kLieShift : !whole ? kLieAcross : r.nvec == s.nv * s.tpr && (s.nv & (s.nv - 1)) == 0 ? kLieFull : kLieWhole;
     P.smem = out_layout(s.slots, s.stages, streams, r.nvec, groups).total;
     return P;
 }

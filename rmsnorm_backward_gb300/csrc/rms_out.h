@@ -43,7 +43,7 @@ struct OutParams {
 
 // shared memory of the ring kernel: ring [slots][stages][1 or 2 rows of nvec
 // vectors] | mbarriers [slots][stages] | sums and maxima [slots][2][2][16] |
-// group maxima [slots][3][groups] | abort flags [slots]
+// group maxima [slots][3][groups] (kLieAcross) | abort flags [slots]
 struct OutLayout {
     size_t bar, red, gmax, flag, total;
 };
@@ -63,7 +63,7 @@ constexpr int kOutThreads = 512;
 constexpr int kShortVectors = 64, kShortElements = 512;
 
 // how rows lie to 16-byte boundaries (rms_out_kernels.cuh)
-enum RowLie : int { kLieFull = 0, kLieWhole = 1, kLieAcross = 2 };
+enum RowLie : int { kLieFull = 0, kLieWhole = 1, kLieAcross = 2, kLieShift = 3 };
 
 // nv: vectors a thread owns (1 to 4; float32 also 6 and 8)
 cudaError_t launch_rms_out_ring(int dtype, int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s);

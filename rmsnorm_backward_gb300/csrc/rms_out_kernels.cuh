@@ -40,6 +40,18 @@ __device__ __forceinline__ float warp_max_nan(float v) {
     return v;
 }
 
+// the maximum over each L neighbouring lanes (16 or 32)
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t b) {
+    if constexpr (L == 32) {
+        b = __reduce_max_sync(0xffffffffu, b);
+    } else {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+    }
+    return b;
+}
+
 // What turns v into a code: code = round(v * quant_factor(a)).  Where a is so
 // small that Q / a would overflow, v is first brought up by 2^100, exactly
 // (`tiny`; the factor is then that of the raised a).  A row (group) of zeros
@@ -97,6 +109,14 @@ template <int KIND>
 __device__ __noinline__ uint32_t quant4_odd(float v0, float v1, float v2, float v3, float a) {
     const float raise = quant_tiny(a) ? kRaise : 1.f, f = quant_factor<KIND>(a);
     return quant4<KIND>((v0 * raise) * f, (v1 * raise) * f, (v2 * raise) * f, (v3 * raise) * f);
+}
+// the same, the first `split` of them of a maximum a0
+template <int KIND>
+__device__ __noinline__ uint32_t quant4_split(float v0, float v1, float v2, float v3, int split, float a0, float a) {
+    const float r0 = quant_tiny(a0) ? kRaise : 1.f, f0 = quant_factor<KIND>(a0);
+    const float r = quant_tiny(a) ? kRaise : 1.f, f = quant_factor<KIND>(a);
+    return quant4<KIND>((v0 * (split > 0 ? r0 : r)) * (split > 0 ? f0 : f), (v1 * (split > 1 ? r0 : r)) * (split > 1 ? f0 : f),
+                        (v2 * (split > 2 ? r0 : r)) * (split > 2 ? f0 : f), (v3 * (split > 3 ? r0 : r)) * (split > 3 ? f0 : f));
 }
 // the codes of a lane's V values (code.x the first four's) by the factor of
 // their maximum a
@@ -252,9 +272,13 @@ cudaError_t rms_out_plain_dispatch(int kind, bool group, const OutParams &p, int
 // refilled; then the outputs are written from registers: x and residual are
 // read once, h is written once and read by nobody.  Bound by HBM: 16384x4096
 // bf16 with the residual 81.7 us, 6.57 TB/s (98% of the measured copy rate);
-// to e4m3 by 128 columns, 8192x16384, 145 us, 6.5 TB/s.  Without the residual
+// to e4m3 by 128 columns, 8192x16384, 144 us, 6.5 TB/s.  Without the residual
 // there are fewer bytes to hide the work of a code behind: 16384x4096 bf16 to
-// e4m3 40 us, 5.0 TB/s, where the warps' instructions bound it.
+// e4m3 36 us, 5.6 TB/s, where the warps' instructions bound it: half the issue
+// slots are used, 4 warps a scheduler wait for one another's latencies.
+// Code counts even where it does not run: with and without a residual in one
+// kernel 46 us against 43 (by 128 columns), the copies of a tensor's end rows
+// inlined 79 against 67 (27711x2202 to int8).
 //
 // How the rows lie (RowLie):
 //  * kLieFull: they start and end on 16 bytes (their codes on V) and are as
@@ -265,11 +289,19 @@ cudaError_t rms_out_plain_dispatch(int kind, bool group, const OutParams &p, int
 //    before and after it that share its first and last 16 bytes (never beyond
 //    the tensor's first and last element: those two ends are copied element by
 //    element); only the vectors that lie wholly in the row are the threads',
-//    and the elements before and after them go to the lanes of the slot's last
-//    warp, one each.  The maxima of groups then meet in shared memory, as
-//    their borders run through vectors.
-// The first two leave out what the third needs: 16384x4096 bf16 to e4m3, without
-// the residual, 67 us as kLieAcross alone, 52 as kLieFull.
+//    so that h and y are stored as vectors, and the elements before and after
+//    them go to the lanes of the slot's last warp, one each.  Borders of
+//    groups then run through vectors, and the groups' maxima meet in shared
+//    memory: one atomic for a group's lanes, one for the elements of its last
+//    vector that another lane owns (10365x6474 f16 to int8 131 us, 3.6 TB/s;
+//    16384x2050 bf16 to e4m3 70 us, 3.4 TB/s; an atomic a vector 171 and 72);
+//  * kLieShift (8-bit outputs without a residual, where nothing is stored at
+//    the rows' own places): copied as kLieAcross, but a thread's vectors are V
+//    columns from the row's first on, put together from two staged ones by
+//    shifts; groups are lanes again, and no element stands alone (27711x2202
+//    to int8 70 us, by 128 columns 82; as kLieAcross 85 and 137).  With a
+//    residual h would have to be shifted back: 16384x2050 by 128 columns 97 us
+//    against 70 as kLieAcross.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ float round_to(float f) {
@@ -284,48 +316,131 @@ __device__ __forceinline__ float round_to(float f) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// Stores a warp's codes, V a lane at consecutive places from `at` of lane 0,
-// of which the first `live` lanes' exist (live > 0).  Where the places do not
-// start on a multiple of V bytes, a lane joins the end of the lane's before
-// it to its own; the warp's first and last bytes, which have no such
-// neighbour, go one to a lane.
+// The 16 bytes from the O-th 32-bit word and `bits` bits on (0 or 16, for
+// 16-bit elements) of two neighbouring vectors.
+template <int V, int O>
+__device__ __forceinline__ uint4 vector_from(uint4 a, uint4 b, int bits) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if constexpr (V == 4) {
+        return make_uint4(w[O], w[O + 1], w[O + 2], w[O + 3]);
+    } else {
+        return make_uint4(__funnelshift_r(w[O], w[O + 1], bits), __funnelshift_r(w[O + 1], w[O + 2], bits),
+                          __funnelshift_r(w[O + 2], w[O + 3], bits), __funnelshift_r(w[O + 3], w[O + 4], bits));
+    }
+}
+// f(O) for the words O of s elements, 0 <= s < V: one uniform branch instead
+// of a choice for each word
+template <int V, typename F>
+__device__ __forceinline__ void by_words(int s, F f) {
+    switch (V == 8 ? s >> 1 : s) {
+        case 0: f(std::integral_constant<int, 0>{}); break;
+        case 1: f(std::integral_constant<int, 1>{}); break;
+        case 2: f(std::integral_constant<int, 2>{}); break;
+        default: f(std::integral_constant<int, 3>{}); break;
+    }
+}
+// the first n of a vector's V elements, zeros for the others
 template <int V>
-__device__ __forceinline__ void store_codes(uint8_t *at, uint2 code, int lane, int live, bool aligned) {
-    uint8_t *p = at + lane * V;
-    if (aligned) {
-        if (lane < live) {
-            if constexpr (V == 8)
-                *reinterpret_cast<uint2 *>(p) = code;
-            else
-                *reinterpret_cast<uint32_t *>(p) = code.x;
+__device__ __forceinline__ uint4 vector_head(uint4 a, int n) {
+    uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (V == 4) {
+            if (i >= n) w[i] = 0;
+        } else {
+            if (2 * i >= n)
+                w[i] = 0;
+            else if (2 * i + 1 >= n)
+                w[i] &= 0xffffu;
         }
-        return;
     }
-    const int m = static_cast<int>(reinterpret_cast<uintptr_t>(at) & (V - 1));
-    uint64_t own = code.x;
-    if constexpr (V == 8) own |= static_cast<uint64_t>(code.y) << 32;
-    const uint64_t prev = __shfl_up_sync(0xffffffffu, own, 1);
-    if (lane > 0 && lane < live) {
-        const uint64_t w = m ? (own << (8 * m)) | (prev >> (8 * (V - m))) : own;
-        if constexpr (V == 8)
-            *reinterpret_cast<uint64_t *>(p - m) = w;
-        else
-            *reinterpret_cast<uint32_t *>(p - m) = static_cast<uint32_t>(w);
-    }
-    // lanes 0 .. V-1: the first lane's bytes below V - m; lanes V .. 2V-1: the
-    // last one's from there
-    const uint64_t end = __shfl_sync(0xffffffffu, own, lane < V ? 0 : live - 1);
-    const int e = lane & (V - 1);
-    if (lane < 2 * V && (lane < V) == (e < V - m)) at[(lane < V ? 0 : (live - 1) * V) + e] = static_cast<uint8_t>(end >> (8 * e));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int KIND, bool GROUP, int NV, int LIE>
+// A warp's codes, V a lane, the bytes [lo, n) of them (lo 0 or V), to
+// consecutive places that start m bytes after a boundary of V: a lane stores
+// the V bytes that end m bytes before its own end, and the bytes at both ends,
+// which fill no such place, go one to a lane.  Out of line: for a row's end
+// vectors only.
+template <int V>
+__device__ __noinline__ void store_codes_part(uint8_t *at, uint2 code, int lane, int lo, int n, int m) {
+    const int place = lane * V - m, first = lo + ((V - m) & (V - 1));
+    const int of = lane < V ? lo + lane : first + ((n - first) & -V) + lane - V;
+    const bool end = lane < 2 * V && of < (lane < V ? min(first, n) : n) && (lane < V || n >= first);
+    const bool vec = place >= lo && place + V <= n;
+    const int from = end ? of / V : 0;
+    uint64_t own = code.x;
+    if constexpr (V == 8) own |= static_cast<uint64_t>(code.y) << 32;
+    const uint64_t prev = __shfl_up_sync(0xffffffffu, own, 1), other = __shfl_sync(0xffffffffu, own, from);
+    const uint64_t w = m ? (own << (8 * m)) | (prev >> (8 * (V - m))) : own;
+    if (vec) {
+        if constexpr (V == 8)
+            *reinterpret_cast<uint64_t *>(at + place) = w;
+        else
+            *reinterpret_cast<uint32_t *>(at + place) = static_cast<uint32_t>(w);
+    }
+    if (end) at[of] = static_cast<uint8_t>(other >> (8 * (of & (V - 1))));
+}
+
+template <int V>
+__device__ __forceinline__ void store_code(uint8_t *at, uint2 code) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2 *>(at) = code;
+    else
+        *reinterpret_cast<uint32_t *>(at) = code.x;
+}
+
+// The same of all 32 V bytes; what depends on m alone is formed once a row.
+template <int V>
+struct CodePlace {
+    int m, bits, from, end;  // end: the lane's byte at an end, or -1
+    __device__ __forceinline__ CodePlace(int lane, int m_) : m(m_) {
+        const int e = lane & (V - 1);
+        bits = 8 * (-m & 3);
+        from = lane < V ? 0 : 31;
+        end = lane < 2 * V && (lane < V) == (e < V - m) ? from * V + e : -1;
+    }
+    __device__ __forceinline__ void store(uint8_t *at, uint2 code, int lane) const {
+        uint8_t *p = at + lane * V;
+        if (m == 0) {
+            store_code<V>(p, code);
+        } else if constexpr (V == 8) {
+            const uint32_t p0 = __shfl_up_sync(0xffffffffu, code.x, 1), p1 = __shfl_up_sync(0xffffffffu, code.y, 1);
+            const uint32_t e0 = __shfl_sync(0xffffffffu, code.x, from), e1 = __shfl_sync(0xffffffffu, code.y, from);
+            const uint32_t w0 = m > 4 ? p0 : p1, w1 = m > 4 ? p1 : code.x, w2 = m > 4 ? code.x : code.y;
+            if (lane > 0)
+                *reinterpret_cast<uint2 *>(p - m) = make_uint2(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits));
+            if (end >= 0) at[end] = static_cast<uint8_t>(__byte_perm(e0, e1, end & 7));
+        } else {
+            const uint32_t p1 = __shfl_up_sync(0xffffffffu, code.x, 1), e0 = __shfl_sync(0xffffffffu, code.x, from);
+            if (lane > 0) *reinterpret_cast<uint32_t *>(p - m) = __funnelshift_r(p1, code.x, bits);
+            if (end >= 0) at[end] = static_cast<uint8_t>(e0 >> (8 * (end & 3)));
+        }
+    }
+};
+
+// Copies to a stage the elements of a tensor's first or last row [s, s + n) of
+// whose first or last 16 bytes some lie outside the tensor; the bytes [x, y)
+// are left for a bulk copy.  Out of line: inlined into the loop over the rows
+// it cost 16% of the kernel's time (2202 columns), for two rows of a tensor.
+template <typename T>
+__device__ __noinline__ uint2 copy_end_row(T *dst, const T *src, const T *base, const T *end, int s, int n, uint32_t bytes) {
+    uint32_t from = 0, to = bytes;
+    if (src < base) from = 16;
+    if (src + bytes / sizeof(T) > end) to = bytes - 16;
+    for (int c = s; c < s + n && c < static_cast<int>(from / sizeof(T)); ++c) dst[c] = src[c];
+    for (int c = max(static_cast<int>(to / sizeof(T)), s); c < s + n; ++c) dst[c] = src[c];
+    return make_uint2(from, to);
+}
+
+template <typename T, int KIND, bool RES, bool GROUP, int NV, int LIE>
 __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutParams p) {
     using Tr = Traits<T>;
     constexpr int V = Tr::kVec;
     constexpr int E = NV * V;
     constexpr bool QUANT = KIND != kOutSame;
-    constexpr bool FULL = LIE == kLieFull, ACROSS = LIE == kLieAcross;
+    constexpr bool FULL = LIE == kLieFull, ACROSS = LIE == kLieAcross, SHIFT = LIE == kLieShift;
+    static_assert(!SHIFT || !RES, "h's vectors are the staged row's");
     constexpr bool GRAW = sizeof(T) == 2 && NV > 3;  // gamma kept in the storage type
     using Out = typename std::conditional<QUANT, uint8_t, T>::type;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -333,8 +448,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const int tid = threadIdx.x, tpr = p.tpr, W = tpr >> 5, slots = p.slots;
     const int slot = tid / tpr, ts = tid - slot * tpr;
     const int warp = ts >> 5, lane = tid & 31;
-    const bool res = QUANT ? p.res != nullptr : true;
-    const int streams = res ? 2 : 1;
+    constexpr int streams = RES ? 2 : 1;
     const bool issuer = warp == 0;
     const int N = p.N, S = p.stages;
     const uint32_t rowb = static_cast<uint32_t>(p.nvec) * 16;
@@ -349,11 +463,18 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const int64_t row_step = (int64_t)p.G * slots, row0 = blockIdx.x * (int64_t)p.cta_step + slot * (int64_t)p.slot_step;
     int64_t row = row0;
     const int ns = slot < slots && row < p.M ? static_cast<int>((p.M - row + row_step - 1) / row_step) : 0;
-    // the row starts s elements into its first vector; vectors [vb, ve) lie
-    // wholly in it
-    const int s = !ACROSS ? 0 : row_shift(blockIdx.x, p.shift0, p.shift_step, V);
-    const int nvec = !ACROSS ? p.nvec : (s + N + V - 1) / V;
-    const int vb = s > 0 ? 1 : 0, ve = (s + N) / V;
+    // the row starts s elements into its first staged vector; the threads'
+    // vectors are [vb, ve): kLieAcross: those that lie wholly in it;
+    // kLieShift: of V columns from the row's first on
+    const int s = !ACROSS && !SHIFT ? 0 : row_shift(blockIdx.x, p.shift0, p.shift_step, V);
+    const int nvec = !ACROSS && !SHIFT ? p.nvec : (s + N + V - 1) / V;
+    const int vb = ACROSS && s > 0 ? 1 : 0, ve = SHIFT ? (N + V - 1) / V : (s + N) / V;
+    // they start at vb; with group maxima to meet at 0, so that a group's
+    // vectors, but for the first s elements of the next group's first, are
+    // those of GL neighbouring lanes
+    constexpr int GL = kQuantGroup / V;
+    const int v_base = meet ? 0 : vb;
+    auto owned = [&](int v) { return FULL || (v < ve && (!meet || v >= vb)); };
     // the lane's element beside them, as a place in the staged row: s <= ce < s + N, or -1
     int ce = -1;
     if (ACROSS && warp == W - 1) {
@@ -368,7 +489,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         fence_barrier_init();
     }
     for (int i = tid; i < slots * 4 * kRedStride; i += kOutThreads) reds[i] = 0.f;
-    if (meet)
+    if constexpr (meet)
         for (int i = tid; i < slots * 3 * groups; i += kOutThreads) reinterpret_cast<uint32_t *>(smem + L.gmax)[i] = 0;
     if (tid < slots) flags[tid] = 0;
     __syncthreads();
@@ -378,23 +499,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     // lane t < streams of the issuing warp copies tensor t's rows
     unsigned char *ring = smem + (size_t)slot * S * streams * rowb;
     uint64_t *bar = bars + slot * S;
-    const T *base = static_cast<const T *>(lane == 0 || !res ? p.x : p.res);
-    const int64_t ld = lane == 0 || !res ? p.ld_x : p.ld_res;
+    const T *base = static_cast<const T *>(lane == 0 || !RES ? p.x : p.res);
+    const int64_t ld = lane == 0 || !RES ? p.ld_x : p.ld_res;
     const T *src = base + row * ld - s;
+    const int end0 = row0 == 0 ? 0 : -1, end1 = ns > 0 && row0 + (ns - 1) * row_step == p.M - 1 ? ns - 1 : -1;
     int issued = 0, pst = 0;
     auto issue = [&]() {
         const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
         uint32_t from = 0, to = bytes;
         unsigned char *dst = ring + (pst * streams + lane) * rowb;
-        const int64_t r = !ACROSS ? 1 : row0 + issued * row_step;
-        if (ACROSS && (r == 0 || r == p.M - 1)) {
+        if ((ACROSS || SHIFT) && (issued == end0 || issued == end1)) {
             // the tensors' first and last rows: nothing outside them is read
             if (lane < streams) {
-                if (src < base) from = 16;
-                if (src + (size_t)nvec * V > base + (p.M - 1) * ld + N) to = bytes - 16;
-                T *d = reinterpret_cast<T *>(dst);
-                for (int c = s; c < s + N && c < static_cast<int>(from / sizeof(T)); ++c) d[c] = src[c];
-                for (int c = max(static_cast<int>(to / sizeof(T)), s); c < s + N; ++c) d[c] = src[c];
+                const uint2 mid = copy_end_row<T>(reinterpret_cast<T *>(dst), src, base, base + (p.M - 1) * ld + N, s, N, bytes);
+                from = mid.x, to = mid.y;
                 if (to > from) mbar_expect_tx(&bar[pst], to - from);
             }
             __syncwarp();
@@ -410,19 +528,19 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     if (issuer)
         while (issued < S && issued < ns) issue();
 
-    const T *gamma = static_cast<const T *>(p.gamma) - s;  // by place in the staged row
+    const T *gamma = static_cast<const T *>(p.gamma) - (ACROSS ? s : 0);
     const bool gvec = (reinterpret_cast<uintptr_t>(gamma) & 15) == 0;
     float gam[GRAW ? 1 : E];
     uint4 graw[GRAW ? NV : 1];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = vb + ts + j * tpr;
+        const int v = v_base + ts + j * tpr;
         float g[V];
-        if ((FULL || v < ve) && gvec) {
+        if ((SHIFT ? (v + 1) * V <= N : owned(v)) && gvec) {
             Tr::unpack(ld_global_nc_v4(gamma + v * V), g);
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) g[e] = FULL || v < ve ? Tr::load1(gamma + v * V + e) : 0.f;
+            for (int e = 0; e < V; ++e) g[e] = (SHIFT ? v * V + e < N : owned(v)) ? Tr::load1(gamma + v * V + e) : 0.f;
         }
         if constexpr (GRAW) {
             graw[j] = Tr::pack(g);
@@ -444,10 +562,26 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const float inv_n = 1.0f / static_cast<float>(N);
     const int in_slot = slot < slots ? slot : 0;
     float *red = reds + in_slot * 4 * kRedStride;
+    // a thread's vectors of a staged row (kLieShift)
+    const bool whole_warp = (ts | 31) + 1 + (NV - 1) * tpr <= N / V;  // none of the warp's beyond the row
+    auto shifted = [&](const unsigned char *row_at, uint4 *a) {
+by_words<V>(s, [&](auto o) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int v = min(ts + j * tpr, ve - 1);
+                a[j] = vector_from<V, decltype(o)::value>(ld_shared_v4(row_at + v * 16),
+                                                          ld_shared_v4(row_at + min(v + 1, nvec - 1) * 16), (s & 1) * 16);
+            }
+        });
+        if (!whole_warp) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) a[j] = vector_head<V>(a[j], N - (ts + j * tpr) * V);
+        }
+    };
     uint32_t *gmax = reinterpret_cast<uint32_t *>(smem + L.gmax) + in_slot * 3 * groups;  // of rows k mod 3
+    int buf = 0;                                                                           // k mod 3
     volatile int *flag = flags + slot;
     RingPos pos;
-    int buf = 0;  // k mod 3
     int k = 0;
     for (; k < ns; ++k, row += row_step) {
         const bool timed_out = !mbar_wait_bounded(&bar[pos.stage], pos.parity);
@@ -457,18 +591,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             issue();
         }
         const unsigned char *sx = ring + pos.stage * streams * rowb;
-        uint32_t *gm = gmax + buf * groups;
-        T *h = static_cast<T *>(p.h) + (res ? row * p.ld_h - s : 0);
+        T *h = static_cast<T *>(p.h) + (RES ? row * p.ld_h - (ACROSS ? s : 0) : 0);
         float sum = 0.f, held[E], he = 0.f;
         float most = 0.f, vmost[GROUP ? NV : 1];  // max |v|, NaN if any is
+        uint4 xs[SHIFT ? NV : 1];
+        if constexpr (SHIFT) shifted(sx, xs);
+        uint32_t *gm = gmax + buf * groups;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = vb + ts + j * tpr;
+            const int v = v_base + ts + j * tpr;
             if constexpr (GROUP) vmost[j] = 0.f;
-            if (FULL || v < ve) {
+            if (SHIFT || owned(v)) {
                 float f[V];
-                Tr::unpack(ld_shared_v4(sx + v * 16), f);
-                if (res) {
+                Tr::unpack(SHIFT ? xs[j] : ld_shared_v4(sx + v * 16), f);
+                if constexpr (RES) {
                     float r[V];
                     Tr::unpack(ld_shared_v4(sx + rowb + v * 16), r);
 #pragma unroll
@@ -497,20 +633,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                     for (int e = 1; e < V; ++e) m = max_nan(m, fabsf(held[j * V + e]));
                     if constexpr (GROUP) {
                         vmost[j] = m;
-                        if (meet) {
-                            const int c0 = v * V - s, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
-                            if (split < V) {  // in two groups
-                                float m1 = m = 0.f;
+                        if (meet && s > 0 && (lane & (GL - 1)) == 0) {  // in two groups
+                            float m1 = m = 0.f;
 #pragma unroll
-                                for (int e = 0; e < V; ++e) {
-                                    if (e < split)
-                                        m = max_nan(m, fabsf(held[j * V + e]));
-                                    else
-                                        m1 = max_nan(m1, fabsf(held[j * V + e]));
-                                }
-                                atomicMax(gm + g + 1, __float_as_uint(m1));
+                            for (int e = 0; e < V; ++e) {
+                                if (e < s)
+                                    m1 = max_nan(m1, fabsf(held[j * V + e]));
+                                else
+                                    m = max_nan(m, fabsf(held[j * V + e]));
                             }
-                            atomicMax(gm + g, __float_as_uint(m));
+                            vmost[j] = m;
+                            atomicMax(gm + v / GL - 1, __float_as_uint(m1));
                         }
                     } else {
                         most = max_nan(most, m);
@@ -523,7 +656,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         }
         if (ACROSS && ce >= 0) {
             he = Tr::load1(reinterpret_cast<const T *>(sx) + ce);
-            if (res) {
+            if constexpr (RES) {
                 he = round_to<T>(he + Tr::load1(reinterpret_cast<const T *>(sx + rowb) + ce));
                 Tr::store1(h + ce, he);
             }
@@ -532,6 +665,13 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 he *= ge;
                 most = max_nan(most, fabsf(he));
                 if (meet) atomicMax(gm + (ce - s) / kQuantGroup, abs_bits(he));
+            }
+        }
+        if constexpr (meet) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t b = lanes_max<GL>(__float_as_uint(vmost[j]));
+                if ((lane & (GL - 1)) == 0 && b != 0) atomicMax(gm + (ts + j * tpr) / GL, b);
             }
         }
         // the exchange: warp sums (and maxima, as bits: the order of the
@@ -558,7 +698,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
             }
             if (*flag) break;
         } else {
-            __syncwarp();  // the group maxima of the warp's lanes
+            __syncwarp();
             if (__any_sync(0xffffffffu, timed_out)) break;
         }
         // the slot has the row in registers: refill its stage
@@ -569,12 +709,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
         float rs = 0.f;
         if (!QUANT || GROUP || ts == 0) rs = __frsqrt_rn(fmaf(sum, inv_n, p.eps));
         if (ts == 0) p.rstd[row] = rs;
-        Out *out = static_cast<Out *>(p.out) + row * p.ld_out - s;
+        Out *out = static_cast<Out *>(p.out) + row * p.ld_out - (ACROSS ? s : 0);
         if constexpr (!QUANT) {
             const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int v = vb + ts + j * tpr;
+                const int v = v_base + ts + j * tpr;
                 if (FULL || v < ve) {
                     float o[V], g[V];
                     gamma_of(j, g);
@@ -595,72 +735,86 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
                 if (ts == 0) p.scale[row] = quant_scale<KIND>(rs, most);
             }
             float *scale = p.scale + (GROUP ? row * groups : 0);
-            if (meet) {
+            if constexpr (meet) {
                 // the maxima of row k-1, read by nobody any more, for row k+2
                 uint32_t *clear = gmax + (buf == 0 ? 2 : buf - 1) * groups;
                 for (int i = ts; i < groups; i += tpr) {
                     clear[i] = 0;
                     scale[i] = quant_scale<KIND>(rs, __uint_as_float(gm[i]));
                 }
+                // Lane j of a group's lanes divides for their vector j, lane
+                // GL/2 + j for the group before it; -1: no ordinary factor.
+                const int j = lane & (GL / 2 - 1), at = (ts - lane) + j * tpr + (lane & ~(GL - 1));
+                const int g = at / GL - ((lane & (GL / 2)) != 0);
+                qf = 1.f;
+                if (j < NV && g >= 0 && g < groups) {
+                    const float m = __uint_as_float(gm[g]);
+                    qf = quant_plain(m) ? quant_factor<KIND>(m) : -1.f;
+                }
             }
-            if constexpr (GROUP && !ACROSS) {
+            if constexpr (GROUP && !meet) {
                 // The maximum of a group from its lanes (16 of a 16-bit type,
                 // 32 of float32); lane j of them divides for their vector j
                 // and writes its scale: one division a row, not one a vector.
-                constexpr int GL = kQuantGroup / V;
                 float mine = 0.f;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    uint32_t b = __float_as_uint(vmost[j]);
-                    if constexpr (GL == 32) {
-                        b = __reduce_max_sync(0xffffffffu, b);
-                    } else {
-#pragma unroll
-                        for (int o = GL / 2; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-                    }
-                    vmost[j] = __uint_as_float(b);
+                    vmost[j] = __uint_as_float(lanes_max<GL>(__float_as_uint(vmost[j])));
                     if ((lane & (GL - 1)) == j) mine = vmost[j];
                 }
                 qf = quant_factor<KIND>(mine);
                 const int at = (ts - lane) + (lane & (GL - 1)) * tpr + (lane & ~(GL - 1));  // its vector
                 if ((lane & (GL - 1)) < NV && at < ve) scale[at / GL] = quant_scale<KIND>(rs, mine);
             }
+            const CodePlace<V> place(lane, (!ACROSS && !SHIFT) || p.codes_aligned ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(out) & (V - 1)));
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int v0 = vb + (ts - lane) + j * tpr, v = v0 + lane;
+                const int v0 = v_base + (ts - lane) + j * tpr;
                 if (!FULL && v0 >= ve) break;  // the whole warp
                 float *t = held + j * V;
                 uint2 code = make_uint2(0, 0);
                 if constexpr (meet) {
-                    // the vector's columns in one group or two
-                    const int c0 = v < ve ? v * V - s : 0, g = c0 / kQuantGroup, split = (g + 1) * kQuantGroup - c0;
-                    const float m = __uint_as_float(gm[g]), f0 = quant_factor<KIND>(m);
-                    const float r0 = quant_tiny(m) ? kRaise : 1.f;
-                    float f1 = f0, r1 = r0;
-                    if (split < V) {
-                        const float m1 = __uint_as_float(gm[g + 1]);
-                        f1 = quant_factor<KIND>(m1), r1 = quant_tiny(m1) ? kRaise : 1.f;
-                    }
+                    // of the first of a group's vectors, s elements are the
+                    // group's before it
+                    const int split = (lane & (GL - 1)) == 0 ? s : 0, of = lane & ~(GL - 1);
+                    const float f = __shfl_sync(0xffffffffu, qf, of + j);
+                    const float f1 = __shfl_sync(0xffffffffu, qf, of + GL / 2 + j), f0 = split ? f1 : f;
+                    if (f > 0.f && f0 > 0.f) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] = (t[e] * (e < split ? r0 : r1)) * (e < split ? f0 : f1);
-                    code.x = quant4<KIND>(t[0], t[1], t[2], t[3]);
-                    if constexpr (V == 8) code.y = quant4<KIND>(t[4], t[5], t[6], t[7]);
+                        for (int i = 0; i < V / 2; ++i) {
+                            const float2 w = pair_mul(pair_at(t, i), make_float2(2 * i < split ? f0 : f,
+                                                                                 2 * i + 1 < split ? f0 : f));
+                            t[2 * i] = w.x, t[2 * i + 1] = w.y;
+                        }
+                        code.x = quant4_finite<KIND>(t);
+                        if constexpr (V == 8) code.y = quant4_finite<KIND>(t + 4);
+                    } else {
+                        const int v = v0 + lane, g = v / GL;
+                        const float a = v < ve ? __uint_as_float(gm[g]) : 1.f;
+                        const float a0 = split && v < ve && g > 0 ? __uint_as_float(gm[g - 1]) : a;
+                        code.x = quant4_split<KIND>(t[0], t[1], t[2], t[3], split, a0, a);
+                        if constexpr (V == 8) code.y = quant4_split<KIND>(t[4], t[5], t[6], t[7], split - 4, a0, a);
+                    }
                 } else if constexpr (GROUP) {
-                    constexpr int GL = kQuantGroup / V;
                     const float f = __shfl_sync(0xffffffffu, qf, (lane & ~(GL - 1)) + j);
                     code = quant_vector<KIND, V>(t, f, vmost[j]);
                 } else {
                     code = quant_vector<KIND, V>(t, qf, most);
                 }
-                store_codes<V>(out + v0 * V, code, lane, FULL || ve - v0 > 32 ? 32 : ve - v0, !ACROSS || p.codes_aligned);
+                if constexpr (!ACROSS && !SHIFT) {
+                    if (FULL || v0 + lane < ve) store_code<V>(out + (v0 + lane) * V, code);
+                } else {
+                    const int lo = meet && v0 < vb ? V : 0, n = SHIFT ? N - v0 * V : (ve - v0) * V;
+                    if (n >= 32 * V && lo == 0)
+                        place.store(out + v0 * V, code, lane);
+                    else
+                        store_codes_part<V>(out + v0 * V, code, lane, lo, min(n, 32 * V), place.m);
+                }
             }
             if (ACROSS && ce >= 0) {
-                if constexpr (GROUP) {
-                    const float a = __uint_as_float(gm[(ce - s) / kQuantGroup]);
-                    out[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * quant_factor<KIND>(a));
-                } else {
-                    out[ce] = quant1<KIND>((he * (quant_tiny(most) ? kRaise : 1.f)) * qf);
-                }
+                const float a = meet ? __uint_as_float(gm[(ce - s) / kQuantGroup]) : most;
+                const float f = meet ? quant_factor<KIND>(a) : qf;
+                out[ce] = quant1<KIND>((he * (quant_tiny(a) ? kRaise : 1.f)) * f);
             }
         }
         buf = buf == 2 ? 0 : buf + 1;
@@ -678,48 +832,58 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     }
 }
 
-template <typename T, int KIND, bool GROUP, int NV, int LIE>
-cudaError_t rms_out_ring_launch(const OutParams &p, size_t smem, cudaStream_t s) {
+template <typename T, int KIND, bool RES, bool GROUP, int NV, int LIE>
+cudaError_t rms_out_ring_start(const OutParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, GROUP, NV, LIE>, done);
+    cudaError_t e = ensure_smem_optin(rms_out_ring_kernel<T, KIND, RES, GROUP, NV, LIE>, done);
     if (e != cudaSuccess) return e;
-    return launch_dependent(rms_out_ring_kernel<T, KIND, GROUP, NV, LIE>, p.G, kOutThreads, smem, s, p);
+    return launch_dependent(rms_out_ring_kernel<T, KIND, RES, GROUP, NV, LIE>, p.G, kOutThreads, smem, s, p);
 }
 
-template <typename T, int KIND, bool GROUP, int NV>
+template <typename T, int KIND, bool RES, bool GROUP, int NV>
 cudaError_t rms_out_ring_lie(int lie, const OutParams &p, size_t smem, cudaStream_t s) {
     if constexpr ((NV & (NV - 1)) == 0) {
-        if (lie == kLieFull) return rms_out_ring_launch<T, KIND, GROUP, NV, kLieFull>(p, smem, s);
+        if (lie == kLieFull) return rms_out_ring_start<T, KIND, RES, GROUP, NV, kLieFull>(p, smem, s);
     }
-    return lie == kLieAcross ? rms_out_ring_launch<T, KIND, GROUP, NV, kLieAcross>(p, smem, s)
-                             : rms_out_ring_launch<T, KIND, GROUP, NV, kLieWhole>(p, smem, s);
+    if (lie == kLieWhole) return rms_out_ring_start<T, KIND, RES, GROUP, NV, kLieWhole>(p, smem, s);
+    // rows across 16-byte boundaries
+    return rms_out_ring_start<T, KIND, RES, GROUP, NV, RES ? kLieAcross : kLieShift>(p, smem, s);
 }
 
-template <typename T, int KIND, bool GROUP>
+template <typename T, int KIND, bool RES, bool GROUP>
 cudaError_t rms_out_ring_nv(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
     switch (nv) {
-        case 1: return rms_out_ring_lie<T, KIND, GROUP, 1>(lie, p, smem, s);
-        case 2: return rms_out_ring_lie<T, KIND, GROUP, 2>(lie, p, smem, s);
-        case 3: return rms_out_ring_lie<T, KIND, GROUP, 3>(lie, p, smem, s);
-        case 4: return rms_out_ring_lie<T, KIND, GROUP, 4>(lie, p, smem, s);
+        case 1: return rms_out_ring_lie<T, KIND, RES, GROUP, 1>(lie, p, smem, s);
+        case 2: return rms_out_ring_lie<T, KIND, RES, GROUP, 2>(lie, p, smem, s);
+        case 3: return rms_out_ring_lie<T, KIND, RES, GROUP, 3>(lie, p, smem, s);
+        case 4: return rms_out_ring_lie<T, KIND, RES, GROUP, 4>(lie, p, smem, s);
     }
     if constexpr (sizeof(T) == 4) {
-        if (nv == 6) return rms_out_ring_lie<T, KIND, GROUP, 6>(lie, p, smem, s);
-        if (nv == 8) return rms_out_ring_lie<T, KIND, GROUP, 8>(lie, p, smem, s);
+        if (nv == 6) return rms_out_ring_lie<T, KIND, RES, GROUP, 6>(lie, p, smem, s);
+        if (nv == 8) return rms_out_ring_lie<T, KIND, RES, GROUP, 8>(lie, p, smem, s);
     }
     return cudaErrorInvalidValue;
 }
 
+template <typename T, int KIND, bool RES>
+cudaError_t rms_out_ring_group(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    if constexpr (KIND != kOutSame) {
+        if (p.group) return rms_out_ring_nv<T, KIND, RES, true>(nv, lie, p, smem, s);
+    }
+    return rms_out_ring_nv<T, KIND, RES, false>(nv, lie, p, smem, s);
+}
+
 template <typename T>
 cudaError_t rms_out_ring_dispatch(int nv, int lie, const OutParams &p, size_t smem, cudaStream_t s) {
+    const bool res = p.res != nullptr;
     switch (p.kind) {
-        case kOutSame: return rms_out_ring_nv<T, kOutSame, false>(nv, lie, p, smem, s);
+        case kOutSame: return res ? rms_out_ring_group<T, kOutSame, true>(nv, lie, p, smem, s) : cudaErrorInvalidValue;
         case kOutE4M3:
-            return p.group ? rms_out_ring_nv<T, kOutE4M3, true>(nv, lie, p, smem, s)
-                           : rms_out_ring_nv<T, kOutE4M3, false>(nv, lie, p, smem, s);
+            return res ? rms_out_ring_group<T, kOutE4M3, true>(nv, lie, p, smem, s)
+                       : rms_out_ring_group<T, kOutE4M3, false>(nv, lie, p, smem, s);
         case kOutInt8:
-            return p.group ? rms_out_ring_nv<T, kOutInt8, true>(nv, lie, p, smem, s)
-                           : rms_out_ring_nv<T, kOutInt8, false>(nv, lie, p, smem, s);
+            return res ? rms_out_ring_group<T, kOutInt8, true>(nv, lie, p, smem, s)
+                       : rms_out_ring_group<T, kOutInt8, false>(nv, lie, p, smem, s);
     }
     return cudaErrorInvalidValue;
 }

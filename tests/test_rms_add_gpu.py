@@ -585,3 +585,50 @@ def test_codes_at_ties(dtype, group):
             q, scale, _, rstd = gbn.rms_add_fwd_q8(x.cuda(), torch.zeros_like(x).cuda(), gamma.cuda(), EPS,
                                                    q_dtype=q_dtype, group=group)
             assert torch.equal(q.cpu().view(torch.uint8), code.view(torch.uint8)), (N, q_dtype)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [517, 1030, 2049, 2055, 4099, 6474])
+def test_codes_of_rows_across_boundaries(N, dtype, group):
+    """The same codes from both kernels at every shift of rows and of codes, with groups of zeros, tiny, infinite and NaN
+    values; bytes between the rows' codes stay as they are."""
+    M = 37 if N > 2100 else 2500  # the latter: several rows to a slot
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(M, N, generator=g).to(DT[dtype])
+    tiny = 6e-8 if dtype == "f16" else 1e-34
+    x[1] = 0
+    x[2, 100:300] = 0
+    x[3, 100:300] = tiny
+    x[4, 130] = float("inf")
+    x[5, 255] = float("nan")
+    x[6, N - 1] = float("-inf")
+    x[7, 0] = float("nan")
+    x[M // 2:M // 2 + 8] = x[:8]
+    x, gamma = x.cuda(), torch.randn(N, generator=g).to(DT[dtype]).cuda()
+    for more, more_q, at in ((0, 0, 0), (1, 1, 0), (2, 0, 1), (5, 3, 3), (8 - N % 8, 8 - N % 8, 0), (8 - N % 8, 8 - N % 8, 4)):
+        def rows(values, start, dt, ld):
+            buf = torch.full((start + M * ld + 8,), 85, dtype=dt, device="cuda")
+            view = buf.as_strided((M, N), (ld, 1), start)
+            if values is not None:
+                view.copy_(values)
+            return buf, view
+
+        _, xs = rows(x, at, DT[dtype], N + more)
+        _, rs = rows(torch.zeros_like(x), at, DT[dtype], N + more)
+        for q_dtype in gbn.Q_DTYPE_CODES:
+            for res in (False, True):
+                got = []
+                for kernel in ("auto", "plain"):
+                    buf, q = rows(None, at, torch.uint8, N + more_q)
+                    if res:
+                        _, h = rows(None, at, DT[dtype], N + more)
+                        out = gbn.rms_add_fwd_q8(xs, rs, gamma, EPS, q_dtype=q_dtype, group=group, q=q.view(q_dtype), h=h,
+                                                 kernel=kernel)
+                        assert torch.equal(torch.nan_to_num(h), torch.nan_to_num(x)), (more, q_dtype, kernel)
+                    else:
+                        out = gbn.rms_fwd_q8(xs, gamma, EPS, q_dtype=q_dtype, group=group, q=q.view(q_dtype), kernel=kernel)
+                    got.append((buf, out[1]))
+                assert torch.equal(got[0][0], got[1][0]), (more, more_q, at, q_dtype, res)
+                # rstd's sum may differ in its last bits: (N + 8) / 2 roundings of 2^-24 at most, halved by the root
+                torch.testing.assert_close(got[0][1], got[1][1], rtol=(N + 8) * 2.0**-25, atol=0, equal_nan=True)
