@@ -184,20 +184,18 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
     const T *base = static_cast<const T *>(lane == 0 ? p.h : lane == 1 ? p.dy : p.dh);
     const int64_t ld = lane == 0 ? p.ld_h : lane == 1 ? p.ld_dy : p.ld_dh;
     const T *src = base + (first + (int64_t)slot * step) * ld - s;
+    const int end0 = first == 0 && slot == 0 ? 0 : -1;
+    const int end1 = ns > 0 && slot + (ns - 1) * slots == nrows - 1 && first + (int64_t)(nrows - 1) * step == p.M - 1 ? ns - 1 : -1;
     int issued = 0, pst = 0;
     auto issue = [&]() {
         const uint32_t bytes = static_cast<uint32_t>(nvec) * 16;
         uint32_t from = 0, to = bytes;
         unsigned char *dst = ring + ((size_t)pst * 3 + lane) * rowb;
-        const int64_t row = SHIFT ? first + (int64_t)(slot + issued * slots) * step : 0;
-        if (SHIFT && (row == 0 || row == p.M - 1)) {
+        if (SHIFT && (issued == end0 || issued == end1)) {
             // the tensors' first and last rows: nothing outside them is read
             if (lane < 3) {
-                if (src < base) from = 16;
-                if (src + (size_t)nvec * V > base + (p.M - 1) * ld + N) to = bytes - 16;
-                T *d = reinterpret_cast<T *>(dst);
-                for (int c = s; c < s + N && c < static_cast<int>(from / sizeof(T)); ++c) d[c] = src[c];
-                for (int c = max(static_cast<int>(to / sizeof(T)), s); c < s + N; ++c) d[c] = src[c];
+                const uint2 mid = copy_end_row<T>(reinterpret_cast<T *>(dst), src, base, base + (p.M - 1) * ld + N, s, N, bytes);
+                from = mid.x, to = mid.y;
                 if (to > from) mbar_expect_tx(&bar[pst], to - from);
             }
             __syncwarp();

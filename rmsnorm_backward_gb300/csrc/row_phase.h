@@ -16,4 +16,19 @@ __host__ __device__ inline int row_shift(int64_t row, int shift0, int shift_step
     return static_cast<int>((shift0 + row * shift_step) & (V - 1));
 }
 
+// Copies to a stage the elements of a tensor's first or last row [s, s + n) of
+// whose first or last 16 bytes some lie outside the tensor; the bytes [x, y)
+// are left for a bulk copy.  Out of line: inlined into the loop over the rows
+// it cost an eighth of the 8-bit forward's time (27711x2202 bf16: 79 us, 67
+// without), for two rows of a tensor.
+template <typename T>
+__device__ __noinline__ uint2 copy_end_row(T *dst, const T *src, const T *base, const T *end, int s, int n, uint32_t bytes) {
+    uint32_t from = 0, to = bytes;
+    if (src < base) from = 16;
+    if (src + bytes / sizeof(T) > end) to = bytes - 16;
+    for (int c = s; c < s + n && c < static_cast<int>(from / sizeof(T)); ++c) dst[c] = src[c];
+    for (int c = max(static_cast<int>(to / sizeof(T)), s); c < s + n; ++c) dst[c] = src[c];
+    return make_uint2(from, to);
+}
+
 }  // namespace gbn
