@@ -290,16 +290,6 @@ __host__ __device__ __forceinline__ void block_rows(int64_t M, int G, int b, int
 
 namespace gbn {
 
-// Floats of reduction scratch per slot: 128, as [buffer][NQ][16 warps].
-constexpr int kRedStride = 16;
-
-// Sums the NQ values of every thread of one row slot (W warps, tpr = 32*W
-// threads, named barrier bar_id) and leaves the totals in v on every thread
-// of the slot: a butterfly within each warp, then the W warp sums added in
-// warp order (read as 16-byte vectors).  `buf` is this slot's scratch of
-// NQ*kRedStride floats; consecutive calls must alternate buffers.  Also
-// returns, uniformly over the slot, whether any of its threads passed
-// give_up = true (a wait that ran out); `flag` is the slot's abort flag.
 // Butterfly sum of two values over the 32 lanes with six shuffles: after the
 // first exchange, lanes 0-15 carry partial sums of v0 and lanes 16-31 of v1;
 // four more butterfly steps finish both (each half's lanes end with the same
@@ -316,42 +306,11 @@ __device__ __forceinline__ void warp_sum2(float &v0, float &v1) {
     v1 = hi ? t : other;
 }
 
-template <int NQ>
-__device__ __forceinline__ bool slot_reduce(float (&v)[NQ], float *buf, volatile int *flag, bool give_up,
-                                            int W, int warp, int lane, int bar_id, int tpr) {
-    if constexpr (NQ == 2) {
-        warp_sum2(v[0], v[1]);
-    } else {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) v[q] = warp_sum(v[q]);
-    }
-    if (W == 1) return __any_sync(0xffffffffu, give_up) != 0;
-    if (give_up) *flag = 1;
-    if (lane == 0) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) buf[q * kRedStride + warp] = v[q];
-    }
-    named_barrier(bar_id, tpr);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-        const float *b = buf + q * kRedStride;
-        if (W == 2) {
-            const float2 t = *reinterpret_cast<const float2 *>(b);
-            v[q] = t.x + t.y;
-        } else {
-            float s = 0.f;
-            for (int w = 0; w < W; w += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(b + w);
-                s = w == 0 ? t.x : s + t.x;
-                s += t.y;
-                s += t.z;
-                s += t.w;
-            }
-            v[q] = s;
-        }
-    }
-    return *flag != 0;
-}
+}  // namespace gbn
+
+#include "slot_exchange.cuh"
+
+namespace gbn {
 
 // Stage ring position of one slot: stage index and the parity of the use of
 // that stage, advanced without division.
