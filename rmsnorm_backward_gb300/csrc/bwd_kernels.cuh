@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
     float *st_rstd = reinterpret_cast<float *>(smem + L.stat_off);
     float *st_mean = st_rstd + p.stat_rows;
     float *red = reinterpret_cast<float *>(smem + L.red_off) + slot * 4 * 2 * kRedStride;
-    volatile uint16_t *flags = reinterpret_cast<uint16_t *>(smem + L.flag_off) + 2 * slot;
+    volatile int *flag = reinterpret_cast<int *>(smem + L.flag_off) + slot;
 
     int64_t row0;
     int nrows;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
         for (int i = 0; i < slots * S; ++i) mbar_init(&all[i], 1);
         fence_barrier_init();
     }
-    if (ts < 2) flags[ts] = 0;
+    if (ts == 0) *flag = 0;
     __syncthreads();
 
     // producer (thread 0 of the slot): the slot's rows in order
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                 float m[1] = {0.f};
 #pragma unroll
                 for (int e = 0; e < E; ++e) m[0] += xv[e];
-                if (slot_reduce<1>(m, red + 6 * kRedStride, flags, 0, timed_out, W, warp, lane, 1 + slot, tpr)) break;
+                if (slot_reduce<1>(m, red + 6 * kRedStride, flag, 2 * k + 1, timed_out, W, warp, lane, 1 + slot, tpr)) break;
                 mu = m[0] * inv_n;
             }
             float r[LN ? 3 : 2];  // sum((x-mean)^2), [sum(dyhat)], sum(dyhat*(x-mean))
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                     r[LN ? 2 : 1] = fmaf(dyhat, d, r[LN ? 2 : 1]);
                 }
             }
-            const bool abort = slot_reduce<LN ? 3 : 2>(r, red + (k & 1) * 3 * kRedStride, flags, LN ? 1 : k,
+            const bool abort = slot_reduce<LN ? 3 : 2>(r, red + (k & 1) * 3 * kRedStride, flag, 2 * k + 2,
                                                        LN ? false : timed_out, W, warp, lane, 1 + slot, tpr);
             if (abort) break;
             if (ts == 0 && issued < ns) {  // the row is in registers: refill its stage
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                     for (int e = 0; e < V; ++e) dyv[j * V + e] = 0.f;
                 }
             }
-            if (slot_reduce<2>(r, red + (k & 1) * 2 * kRedStride, flags, k, timed_out, W, warp, lane, 1 + slot, tpr))
+            if (slot_reduce<2>(r, red + (k & 1) * 2 * kRedStride, flag, k + 1, timed_out, W, warp, lane, 1 + slot, tpr))
                 break;
             if (ts == 0 && issued < ns) {  // the row is in registers: refill its stage
                 fence_proxy_async();
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                     for (int e = 0; e < V; ++e) q[0] = LN ? q[0] + f[e] : fmaf(f[e], f[e], q[0]);
                 }
             }
-            if (slot_reduce<1>(q, red + 4 * kRedStride, flags, 0, timed_out, W, warp, lane, 1 + slot, tpr)) break;
+            if (slot_reduce<1>(q, red + 4 * kRedStride, flag, 3 * k + 1, timed_out, W, warp, lane, 1 + slot, tpr)) break;
             if constexpr (LN) {
                 mu = q[0] * inv_n;
                 float c[1] = {0.f};
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                         }
                     }
                 }
-                slot_reduce<1>(c, red + 5 * kRedStride, flags, 0, false, W, warp, lane, 1 + slot, tpr);
+                slot_reduce<1>(c, red + 5 * kRedStride, flag, 3 * k + 2, false, W, warp, lane, 1 + slot, tpr);
                 rs = 1.0f / sqrtf(c[0] * inv_n + p.eps);
             } else {
                 rs = 1.0f / sqrtf(q[0] * inv_n + p.eps);
@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) bwd_staged_kernel(const BwdPa
                 if constexpr (HOLD) dh[j * V + e] = dyhat;
             }
         }
-        const bool abort = slot_reduce<2>(s, red + (k & 1) * 2 * kRedStride, flags, RECOMP ? 1 : k, timed_out, W, warp,
-                                          lane, 1 + slot, tpr);
+        const bool abort = slot_reduce<2>(s, red + (k & 1) * 2 * kRedStride, flag, RECOMP ? 3 * k + 3 : k + 1, timed_out, W,
+                                          warp, lane, 1 + slot, tpr);
         if (abort) break;
         // HOLD: the slot is done with this stage; otherwise it re-reads this
         // stage in pass 2 and the previous stage is the one now free

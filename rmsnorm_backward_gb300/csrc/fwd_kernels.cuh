@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) fwd_staged_kernel(const FwdPa
     unsigned char *ring = smem + L.ring_off + (size_t)slot * S * rowb;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L.bar_off) + slot * S;
     float *red = reinterpret_cast<float *>(smem + L.red_off) + slot * 4 * 2 * kRedStride;
-    volatile uint16_t *flags = reinterpret_cast<uint16_t *>(smem + L.flag_off) + 2 * slot;
+    volatile int *flag = reinterpret_cast<int *>(smem + L.flag_off) + slot;
 
     int64_t row0;
     int nrows;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) fwd_staged_kernel(const FwdPa
         for (int i = 0; i < slots * S; ++i) mbar_init(&all[i], 1);
         fence_barrier_init();
     }
-    if (ts < 2) flags[ts] = 0;
+    if (ts == 0) *flag = 0;
     __syncthreads();
 
     const size_t row_step = (size_t)slots * p.ld_y;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) fwd_staged_kernel(const FwdPa
             }
             if constexpr (!HOLD) xr[j] = raw;
         }
-        const bool abort = slot_reduce<1>(sum, red + (k & 1) * 2 * 2 * kRedStride, flags, k, timed_out, W, warp, lane,
+        const bool abort = slot_reduce<1>(sum, red + (k & 1) * 2 * 2 * kRedStride, flag, 2 * k + 1, timed_out, W, warp, lane,
                                           1 + slot, tpr);
         if (abort) break;
         // the slot has the row in registers: refill its stage
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) fwd_staged_kernel(const FwdPa
                     sq[0] = fmaf(d, d, sq[0]);
                 }
             }
-            slot_reduce<1>(sq, red + ((k & 1) * 2 + 1) * 2 * kRedStride, flags, k, false, W, warp, lane, 1 + slot, tpr);
+            slot_reduce<1>(sq, red + ((k & 1) * 2 + 1) * 2 * kRedStride, flag, 2 * k + 2, false, W, warp, lane, 1 + slot, tpr);
             rs = 1.0f / sqrtf(sq[0] * inv_n + p.eps);
         } else {
             rs = 1.0f / sqrtf(sum[0] * inv_n + p.eps);

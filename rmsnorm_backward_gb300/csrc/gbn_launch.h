@@ -77,7 +77,7 @@ struct RingLayout {
     size_t bar_off;               // [slots][stages] mbarriers
     size_t stat_off;              // [stat_rows] rstd, then [stat_rows] mean (LayerNorm)
     size_t red_off;               // [slots][4 buffers][2][kRedStride = 16] floats
-    size_t flag_off;              // [slots][2] 16-bit flags: the slot gives up (slot_meet)
+    size_t flag_off;              // [slots] ints: per-slot abort flags
     size_t total;
 };
 

@@ -37,7 +37,7 @@ struct AddBwdParams {
 // shared memory of the ring kernel: ring [slots][stages][3 rows of nvec
 // vectors], reused for the combine of the slots' partial sums | gamma's
 // vectors, where they are kept there | mbarriers [slots][stages] | rstd
-// [stat_rows] | reduction scratch [slots][2][16] | give-up flags [slots][2]
+// [stat_rows] | reduction scratch [slots][2][16] | abort flags [slots]
 struct AddBwdLayout {
     size_t gam, bar, stat, red, flag, total;
 };

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar);
     float *st_rstd = reinterpret_cast<float *>(smem + L.stat);
     float *reds = reinterpret_cast<float *>(smem + L.red);
-    uint16_t *flags = reinterpret_cast<uint16_t *>(smem + L.flag);
+    int *flags = reinterpret_cast<int *>(smem + L.flag);
 
     // this CTA's rows: first + step*i for i < nrows, all of one phase; the
     // slot's: i = slot + k*slots
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
         fence_barrier_init();
     }
     for (int i = tid; i < slots * 2 * kRedStride; i += kAddBwdThreads) reds[i] = 0.f;
-    if (tid < 2 * slots) flags[tid] = 0;
+    if (tid < slots) flags[tid] = 0;
     __syncthreads();
     griddep_wait();  // whatever is before this kernel on the stream
 
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
 
     const float inv_n = 1.0f / static_cast<float>(N);
     float *red = reds + (slot < slots ? slot : 0) * 2 * kRedStride;
-    volatile uint16_t *flag = flags + 2 * slot;
+    volatile int *flag = flags + slot;
     // vector v of gamma, as pairs' source
     auto gamma_of = [&](int j, int v, float *g) {
         if constexpr (GFLT) {
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kAddBwdThreads, 1) rms_add_bwd_ring_kernel(con
             ee = Tr::load1(reinterpret_cast<const T *>(sh + 2 * rowb) + ce);
             sum[0] = fmaf(de * ge, he, sum[0]);
         }
-        if (slot_reduce<1>(sum, red + (k & 1) * kRedStride, flag, k, timed_out, W, warp, lane, 1 + slot, tpr)) break;
+        if (slot_reduce<1>(sum, red + (k & 1) * kRedStride, flag, k + 1, timed_out, W, warp, lane, 1 + slot, tpr)) break;
         // the slot is done with this row's stage (the row before's): refill it
         if (issuer && issued < ns && (HOLD || k > 0)) {
             fence_proxy_async();

@@ -43,7 +43,7 @@ struct OutParams {
 
 // shared memory of the ring kernel: ring [slots][stages][1 or 2 rows of nvec
 // vectors] | mbarriers [slots][stages] | sums and maxima [slots][2][2][16] |
-// group maxima [slots][3][groups] (kLieAcross) | give-up flags [slots][2]
+// group maxima [slots][3][groups] (kLieAcross) | abort flags [slots]
 struct OutLayout {
     size_t bar, red, gmax, flag, total;
 };

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     const OutLayout L = out_layout(slots, S, streams, p.nvec, meet ? groups : 0);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar);
     float *reds = reinterpret_cast<float *>(smem + L.red);
-    uint16_t *flags = reinterpret_cast<uint16_t *>(smem + L.flag);
+    int *flags = reinterpret_cast<int *>(smem + L.flag);
 
     // the slot's rows: row + k*row_step for k < ns; a CTA's have one shift
     const int64_t row_step = (int64_t)p.G * slots, row0 = blockIdx.x * (int64_t)p.cta_step + slot * (int64_t)p.slot_step;
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     for (int i = tid; i < slots * 4 * kRedStride; i += kOutThreads) reds[i] = 0.f;
     if constexpr (meet)
         for (int i = tid; i < slots * 3 * groups; i += kOutThreads) reinterpret_cast<uint32_t *>(smem + L.gmax)[i] = 0;
-    if (tid < 2 * slots) flags[tid] = 0;
+    if (tid < slots) flags[tid] = 0;
     __syncthreads();
     griddep_wait();  // whatever is before this kernel on the stream
     griddep_launch_dependents();
@@ -566,7 +566,7 @@ by_words<V>(s, [&](auto o) {
     };
     uint32_t *gmax = reinterpret_cast<uint32_t *>(smem + L.gmax) + in_slot * 3 * groups;  // of rows k mod 3
     int buf = 0;                                                                           // k mod 3
-    volatile uint16_t *flag = flags + 2 * slot;
+    volatile int *flag = flags + slot;
     RingPos pos;
     int k = 0;
     for (; k < ns; ++k, row += row_step) {
@@ -671,7 +671,7 @@ by_words<V>(s, [&](auto o) {
                 b[warp] = sum;
                 if constexpr (QUANT && !GROUP) b[kRedStride + warp] = __uint_as_float(bits);
             }
-            const bool stop = slot_meet(flag, k, timed_out, 1 + slot, tpr);
+            slot_meet(flag, k + 1, timed_out, 1 + slot, tpr);
             sum = 0.f;
             for (int w = 0; w < W; w += 4) {
                 const float4 t = *reinterpret_cast<const float4 *>(b + w);
@@ -681,7 +681,7 @@ by_words<V>(s, [&](auto o) {
                     bits = max(max(max(bits, m.x), max(m.y, m.z)), m.w);
                 }
             }
-            if (stop) break;
+            if (slot_stops(flag, k + 1)) break;
         } else {
             __syncwarp();
             if (__any_sync(0xffffffffu, timed_out)) break;

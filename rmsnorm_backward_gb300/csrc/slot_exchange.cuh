@@ -11,28 +11,30 @@ namespace gbn {
 // Floats of reduction scratch per slot: 128, as [buffer][NQ][16 warps].
 constexpr int kRedStride = 16;
 
-// The slot's barrier.  Returns, uniformly over the slot, whether any of its
-// threads came with give_up = true (a wait that ran out).  `flags` are the
-// slot's two, zero at first; of the meetings in which a thread may give up, those
-// that follow one another have rounds of alternating parity.  A warp that is through the barrier of one round may
-// give up in the next before a slower one has read its flag, so that one is
-// another flag; it is written again a round later, behind a barrier that the
-// slower warp reaches after its read.  (With one flag for all rounds the slower
-// warp left a row early, and the others waited at a barrier that never filled.)
-__device__ __forceinline__ bool slot_meet(volatile uint16_t *flags, int round, bool give_up, int bar_id, int tpr) {
-    if (give_up) flags[round & 1] = 1;
+// The slot's barrier.  Behind it slot_stops() says, uniformly over the slot,
+// whether any of its threads came with give_up = true (a wait that ran out).
+// `flag` is the slot's, zero at first; `round` is the meeting's own number, from
+// 1 on and rising.  The flag holds the round in which a warp gave up: a warp that
+// is through one round's barrier may give up in the next before a slower warp
+// has read the flag, which then finds another round's number there and comes to
+// that round's barrier as well.  Nothing writes over a number before all have
+// read it: whoever is through that round's barrier stops there.  (With a mere 1 in the flag
+// the slower warp left a row early, and the others waited at a barrier that
+// never filled.)
+__device__ __forceinline__ void slot_meet(volatile int *flag, int round, bool give_up, int bar_id, int tpr) {
+    if (give_up) *flag = round;
     named_barrier(bar_id, tpr);
-    return flags[round & 1] != 0;
 }
+__device__ __forceinline__ bool slot_stops(const volatile int *flag, int round) { return *flag == round; }
 
 // Sums the NQ values of every thread of one row slot (W warps, tpr = 32*W
 // threads, named barrier bar_id) and leaves the totals in v on every thread
 // of the slot: a butterfly within each warp, then the W warp sums added in
 // warp order (read as 16-byte vectors).  `buf` is this slot's scratch of
 // NQ*kRedStride floats; consecutive calls must alternate buffers.  Returns
-// slot_meet()'s, with its flags and round.
+// slot_stops(), with slot_meet()'s flag and round.
 template <int NQ>
-__device__ __forceinline__ bool slot_reduce(float (&v)[NQ], float *buf, volatile uint16_t *flags, int round,
+__device__ __forceinline__ bool slot_reduce(float (&v)[NQ], float *buf, volatile int *flag, int round,
                                             bool give_up, int W, int warp, int lane, int bar_id, int tpr) {
     if constexpr (NQ == 2) {
         warp_sum2(v[0], v[1]);
@@ -45,7 +47,7 @@ __device__ __forceinline__ bool slot_reduce(float (&v)[NQ], float *buf, volatile
 #pragma unroll
         for (int q = 0; q < NQ; ++q) buf[q * kRedStride + warp] = v[q];
     }
-    const bool stop = slot_meet(flags, round, give_up, bar_id, tpr);
+    slot_meet(flag, round, give_up, bar_id, tpr);
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
         const float *b = buf + q * kRedStride;
@@ -64,7 +66,7 @@ __device__ __forceinline__ bool slot_reduce(float (&v)[NQ], float *buf, volatile
             v[q] = s;
         }
     }
-    return stop;
+    return slot_stops(flag, round);
 }
 
 }  // namespace gbn

@@ -78,7 +78,7 @@ static std::vector<int> run(bool reduce, int W, int rows, int slow, int who, int
     alignas(16) static float buf[2][gbn::kRedStride];
     for (auto &b : buf)
         for (float &f : b) f = 0.f;
-    uint16_t flags[2] = {0, 0};
+    int flag = 0;
     std::vector<int> at(W, rows);
     std::vector<std::thread> t;
     for (int w = 0; w < W; ++w)
@@ -87,8 +87,13 @@ static std::vector<int> run(bool reduce, int W, int rows, int slow, int who, int
             for (int k = 0; k < rows; ++k) {
                 const bool give_up = w == who && k == when;
                 float v[1] = {static_cast<float>(w + 1)};
-                const bool stop = reduce ? gbn::slot_reduce<1>(v, buf[k & 1], flags, k, give_up, W, w, 0, 1, 32 * W)
-                                         : gbn::slot_meet(flags, k, give_up, 1, 32 * W);
+                bool stop;
+                if (reduce) {
+                    stop = gbn::slot_reduce<1>(v, buf[k & 1], &flag, k + 1, give_up, W, w, 0, 1, 32 * W);
+                } else {
+                    gbn::slot_meet(&flag, k + 1, give_up, 1, 32 * W);
+                    stop = gbn::slot_stops(&flag, k + 1);
+                }
                 if (stop || (reduce && v[0] != W * (W + 1) / 2)) {
                     at[w] = k;
                     break;
