@@ -211,6 +211,26 @@ def _stream(device, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(make, *args, device, stream, **kw) -> torch.Tensor:
+    """``make(*args, device=device, **kw)`` for a call on ``stream``.
+
+    On a stream other than the current one the memory is that stream's: the
+    allocator gives it out, and a fill runs, behind what that stream has
+    queued.  (From the current stream's memory it could be a block that work
+    queued there still uses, a workspace that has just been let go above all.)
+    The caller goes on with the result on the current stream, so it is in use
+    there too until it is let go."""
+    if stream is None:
+        return make(*args, device=device, **kw)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # 0 and 1 are the default stream's
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(*args, device=device, **kw)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def bwd_workspace_bytes(M: int, N: int, dtype: torch.dtype, has_beta: bool, device=None) -> int:
     """Workspace bytes the backward needs on ``device`` (default: current)."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
@@ -255,9 +275,9 @@ def ln_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps: float,
     x may be a 2-D view with contiguous rows (any row stride); y likewise.
     kernel: "auto", or "slot" / "plain" to force that kernel (KERNELS)."""
     M, N, ld_x = _rows_ld(x, "x")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-    mean = torch.empty(M, dtype=torch.float32, device=x.device) if mean is None else mean
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    y = _new(torch.empty, x.shape, dtype=x.dtype, device=x.device, stream=stream) if y is None else y
+    mean = _new(torch.empty, M, dtype=torch.float32, device=x.device, stream=stream) if mean is None else mean
+    rstd = _new(torch.empty, M, dtype=torch.float32, device=x.device, stream=stream) if rstd is None else rstd
     for name, t in (("gamma", gamma), ("beta", beta)):
         _vec(t, name, N, x.dtype, x.device)
     _vec(mean, "mean", M, torch.float32, x.device)
@@ -274,8 +294,8 @@ def rms_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, y: Optional[tor
             rstd: Optional[torch.Tensor] = None, kernel: str = "auto", stream=None):
     """RMSNorm forward over the last dimension. Returns (y, rstd)."""
     M, N, ld_x = _rows_ld(x, "x")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    y = _new(torch.empty, x.shape, dtype=x.dtype, device=x.device, stream=stream) if y is None else y
+    rstd = _new(torch.empty, M, dtype=torch.float32, device=x.device, stream=stream) if rstd is None else rstd
     _vec(gamma, "gamma", N, x.dtype, x.device)
     _vec(rstd, "rstd", M, torch.float32, x.device)
     ld_y = _same_rows(y, x, "y")
@@ -286,29 +306,29 @@ def rms_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, y: Optional[tor
     return y, rstd
 
 
-def _bwd_args(dy, x, gamma, stats, dx):
+def _bwd_args(dy, x, gamma, stats, dx, stream):
     M, N, ld_x = _rows_ld(x, "x")
     ld_dy = _same_rows(dy, x, "dy")
     _vec(gamma, "gamma", N, x.dtype, x.device)
     for name, t in stats:
         _vec(t, name, M, torch.float32, x.device)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    dx = _new(torch.empty, x.shape, dtype=x.dtype, device=x.device, stream=stream) if dx is None else dx
     ld_dx = _same_rows(dx, x, "dx")
     return M, N, dx, (ld_x, ld_dy, ld_dx)
 
 
-def _workspace(workspace, M, N, x, ln):
+def _workspace(workspace, M, N, x, ln, stream):
     need = bwd_workspace_bytes(M, N, x.dtype, ln, x.device)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        workspace = _new(torch.empty, max(need, 1), dtype=torch.uint8, device=x.device, stream=stream)
     if workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on x's device")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _grads(t, name, N, grad_dtype, device, accumulate):
+def _grads(t, name, N, grad_dtype, device, accumulate, stream):
     if t is None:
-        return (torch.zeros if accumulate else torch.empty)(N, dtype=grad_dtype, device=device)
+        return _new(torch.zeros if accumulate else torch.empty, N, dtype=grad_dtype, device=device, stream=stream)
     _vec(t, name, N, grad_dtype, device)
     return t
 
@@ -342,10 +362,10 @@ def ln_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: Optiona
     if grad_dtype not in (torch.float32, x.dtype):
         raise ValueError("grad_dtype must be float32 or x's dtype")
     eps_arg = _recompute_eps((mean, rstd), eps)
-    M, N, dx, (ld_x, ld_dy, ld_dx) = _bwd_args(dy, x, gamma, (("mean", mean), ("rstd", rstd)), dx)
-    dgamma = _grads(dgamma, "dgamma", N, grad_dtype, x.device, accumulate)
-    dbeta = _grads(dbeta, "dbeta", N, grad_dtype, x.device, accumulate)
-    workspace, wsb = _workspace(workspace, M, N, x, True)
+    M, N, dx, (ld_x, ld_dy, ld_dx) = _bwd_args(dy, x, gamma, (("mean", mean), ("rstd", rstd)), dx, stream)
+    dgamma = _grads(dgamma, "dgamma", N, grad_dtype, x.device, accumulate, stream)
+    dbeta = _grads(dbeta, "dbeta", N, grad_dtype, x.device, accumulate, stream)
+    workspace, wsb = _workspace(workspace, M, N, x, True, stream)
     opt = _options(ld_x, ld_dy, ld_dx, accumulate, grad_dtype, reduce, kernel, 0, wait_limit_ns)
     with torch.cuda.device(x.device):
         _check("ln_bwd", lib().ln_bwd_ex(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
@@ -363,9 +383,9 @@ def rms_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, rstd: Option
     if grad_dtype not in (torch.float32, x.dtype):
         raise ValueError("grad_dtype must be float32 or x's dtype")
     eps_arg = _recompute_eps((rstd,), eps)
-    M, N, dx, (ld_x, ld_dy, ld_dx) = _bwd_args(dy, x, gamma, (("rstd", rstd),), dx)
-    dgamma = _grads(dgamma, "dgamma", N, grad_dtype, x.device, accumulate)
-    workspace, wsb = _workspace(workspace, M, N, x, False)
+    M, N, dx, (ld_x, ld_dy, ld_dx) = _bwd_args(dy, x, gamma, (("rstd", rstd),), dx, stream)
+    dgamma = _grads(dgamma, "dgamma", N, grad_dtype, x.device, accumulate, stream)
+    workspace, wsb = _workspace(workspace, M, N, x, False, stream)
     opt = _options(ld_x, ld_dy, ld_dx, accumulate, grad_dtype, reduce, kernel, 0, wait_limit_ns)
     with torch.cuda.device(x.device):
         _check("rms_bwd", lib().rms_bwd_ex(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(rstd), _ptr(dx), _ptr(dgamma),
@@ -376,10 +396,10 @@ def rms_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, rstd: Option
 
 def ln_bwd_rows(dy, x, gamma, mean, rstd, *, dx=None, workspace, stream=None):
     """Phase 1 of ln_bwd: dx and the per-CTA partial rows in ``workspace``. Returns dx."""
-    M, N, dx, lds = _bwd_args(dy, x, gamma, (("mean", mean), ("rstd", rstd)), dx)
+    M, N, dx, lds = _bwd_args(dy, x, gamma, (("mean", mean), ("rstd", rstd)), dx, stream)
     if lds != (N, N, N):
         raise ValueError("the backward phases take contiguous rows")
-    workspace, wsb = _workspace(workspace, M, N, x, True)
+    workspace, wsb = _workspace(workspace, M, N, x, True, stream)
     with torch.cuda.device(x.device):
         _check("ln_bwd_rows", lib().ln_bwd_rows(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
                                                 _ptr(dx), M, N, _code(x), _ptr(workspace), wsb,
@@ -389,10 +409,10 @@ def ln_bwd_rows(dy, x, gamma, mean, rstd, *, dx=None, workspace, stream=None):
 
 def rms_bwd_rows(dy, x, gamma, rstd, *, dx=None, workspace, stream=None):
     """Phase 1 of rms_bwd: dx and the per-CTA partial rows in ``workspace``. Returns dx."""
-    M, N, dx, lds = _bwd_args(dy, x, gamma, (("rstd", rstd),), dx)
+    M, N, dx, lds = _bwd_args(dy, x, gamma, (("rstd", rstd),), dx, stream)
     if lds != (N, N, N):
         raise ValueError("the backward phases take contiguous rows")
-    workspace, wsb = _workspace(workspace, M, N, x, False)
+    workspace, wsb = _workspace(workspace, M, N, x, False, stream)
     with torch.cuda.device(x.device):
         _check("rms_bwd_rows", lib().rms_bwd_rows(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(rstd), _ptr(dx), M, N,
                                                   _code(x), _ptr(workspace), wsb, _stream(x.device, stream)))
@@ -419,7 +439,7 @@ def _act_bwd(fn: str, dy: torch.Tensor, preact: torch.Tensor, dx: Optional[torch
         raise ValueError(f"{fn}: dy and preact must match in shape, dtype and device")
     code = _code(dy)
     if dx is None:
-        dx = torch.empty_like(dy)
+        dx = _new(torch.empty_like, dy, device=dy.device, stream=stream)
     elif not dx.is_contiguous() or dx.shape != dy.shape or dx.dtype != dy.dtype or dx.device != dy.device:
         raise ValueError(f"{fn}: dx must be a contiguous tensor like dy")
     dev = dy.device
@@ -450,11 +470,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _f32 = torch.float32
 
 
-def _enqueue(fn: str, device, stream, args, owned=()) -> None:
-    """Calls the library's ``fn(*args, stream)`` with ``device`` current.
-    owned: tensors allocated for this call; where it runs on another stream
-    than the one they were allocated on, their memory stays theirs until that
-    stream is done with it."""
+def _enqueue(fn: str, device, stream, args) -> None:
+    """Calls the library's ``fn(*args, stream)`` with ``device`` current."""
     call = getattr(_lib or lib(), fn)
     if stream is None and _raw_stream is not None:
         handle = _raw_stream(device.index)
@@ -467,11 +484,6 @@ def _enqueue(fn: str, device, stream, args, owned=()) -> None:
             status = call(*args, handle)
     if status != GBN_OK:
         raise GbnError(fn, status)
-    if stream is not None and owned:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        for t in owned:
-            t.record_stream(stream)
 
 
 def _rows_like(t: torch.Tensor, name: str, shape, dtype, device) -> int:
@@ -486,10 +498,10 @@ def _vec_like(t: torch.Tensor, name: str, n: int, dtype, device) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
 
 
-def _new(shape, dtype, device, owned) -> torch.Tensor:
-    t = torch.empty(shape, dtype=dtype, device=device)
-    owned.append(t)
-    return t
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _new(torch.empty, shape, dtype=dtype, device=device, stream=stream)
 
 
 def rms_add_fwd(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, eps: float, *,
@@ -502,31 +514,31 @@ def rms_add_fwd(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor, ep
     Row tensors may be 2-D views with contiguous rows.  kernel: "auto" or
     "plain"."""
     M, N, ld_x = _rows_ld(x, "x")
-    shape, dtype, device, owned = x.shape, x.dtype, x.device, []
+    shape, dtype, device = x.shape, x.dtype, x.device
     ld_r = _rows_like(residual, "residual", shape, dtype, device)
     _vec_like(gamma, "gamma", N, dtype, device)
-    y = _new(shape, dtype, device, owned) if y is None else y
-    h = _new(shape, dtype, device, owned) if h is None else h
-    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
+    y = _empty(shape, dtype, device, stream) if y is None else y
+    h = _empty(shape, dtype, device, stream) if h is None else h
+    rstd = _empty(M, _f32, device, stream) if rstd is None else rstd
     ld_y, ld_h = _rows_like(y, "y", shape, dtype, device), _rows_like(h, "h", shape, dtype, device)
     _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_add_fwd", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), y.data_ptr(), h.data_ptr(), rstd.data_ptr(),
-              eps, M, N, _code(x), ld_x, ld_r, ld_y, ld_h, _ROW_KERNELS[kernel]), owned)
+              eps, M, N, _code(x), ld_x, ld_r, ld_y, ld_h, _ROW_KERNELS[kernel]))
     return y, h, rstd
 
 
-def _q8_args(shape, device, q_dtype, group, q, scale, owned):
+def _q8_args(shape, device, q_dtype, group, q, scale, stream):
     if q is not None:
         q_dtype = q.dtype
     if q_dtype not in Q_DTYPE_CODES:
         raise ValueError(f"q_dtype must be one of {sorted(map(str, Q_DTYPE_CODES))}")
     if group != 0 and group != QUANT_GROUP:
         raise ValueError(f"group must be 0 (a scale for each row) or {QUANT_GROUP}")
-    q = _new(shape, q_dtype, device, owned) if q is None else q
+    q = _empty(shape, q_dtype, device, stream) if q is None else q
     ld_q = _rows_like(q, "q", shape, q_dtype, device)
     scales = shape[:-1] + ((shape[-1] + QUANT_GROUP - 1) // QUANT_GROUP,) if group else shape[:-1]
-    scale = _new(scales, _f32, device, owned) if scale is None else scale
+    scale = _empty(scales, _f32, device, stream) if scale is None else scale
     if scale.shape != scales or scale.dtype is not _f32 or scale.get_device() != device.index or not scale.is_contiguous():
         raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(scales)} on {device}")
     return q, ld_q, scale, Q_DTYPE_CODES[q_dtype]
@@ -542,14 +554,14 @@ def rms_fwd_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, *, q_dtype=torc
     each 128 columns, shape x.shape[:-1] + (ceil(N / 128),).  A given q decides
     q_dtype.  kernel: "auto" or "plain"."""
     M, N, ld_x = _rows_ld(x, "x")
-    device, owned = x.device, []
+    device = x.device
     _vec_like(gamma, "gamma", N, x.dtype, device)
-    q, ld_q, scale, q_code = _q8_args(x.shape, device, q_dtype, group, q, scale, owned)
-    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
+    q, ld_q, scale, q_code = _q8_args(x.shape, device, q_dtype, group, q, scale, stream)
+    rstd = _empty(M, _f32, device, stream) if rstd is None else rstd
     _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_fwd_q8", device, stream,
              (x.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), eps, M, N, _code(x),
-              q_code, group, ld_x, ld_q, _ROW_KERNELS[kernel]), owned)
+              q_code, group, ld_x, ld_q, _ROW_KERNELS[kernel]))
     return q, scale, rstd
 
 
@@ -561,18 +573,17 @@ def rms_add_fwd_q8(x: torch.Tensor, residual: torch.Tensor, gamma: torch.Tensor,
 
     h as in rms_add_fwd (it may be x or residual), the rest as in rms_fwd_q8."""
     M, N, ld_x = _rows_ld(x, "x")
-    shape, dtype, device, owned = x.shape, x.dtype, x.device, []
+    shape, dtype, device = x.shape, x.dtype, x.device
     ld_r = _rows_like(residual, "residual", shape, dtype, device)
     _vec_like(gamma, "gamma", N, dtype, device)
-    q, ld_q, scale, q_code = _q8_args(shape, device, q_dtype, group, q, scale, owned)
-    h = _new(shape, dtype, device, owned) if h is None else h
-    rstd = _new(M, _f32, device, owned) if rstd is None else rstd
+    q, ld_q, scale, q_code = _q8_args(shape, device, q_dtype, group, q, scale, stream)
+    h = _empty(shape, dtype, device, stream) if h is None else h
+    rstd = _empty(M, _f32, device, stream) if rstd is None else rstd
     ld_h = _rows_like(h, "h", shape, dtype, device)
     _vec_like(rstd, "rstd", M, _f32, device)
     _enqueue("rms_add_fwd_q8", device, stream,
              (x.data_ptr(), residual.data_ptr(), gamma.data_ptr(), q.data_ptr(), scale.data_ptr(), h.data_ptr(),
-              rstd.data_ptr(), eps, M, N, _code(x), q_code, group, ld_x, ld_r, ld_q, ld_h, _ROW_KERNELS[kernel]),
-             owned)
+              rstd.data_ptr(), eps, M, N, _code(x), q_code, group, ld_x, ld_r, ld_q, ld_h, _ROW_KERNELS[kernel]))
     return q, scale, h, rstd
 
 
@@ -587,21 +598,20 @@ def rms_add_bwd(dy: torch.Tensor, dh: torch.Tensor, h: torch.Tensor, gamma: torc
     accumulate, grad_dtype and workspace as for rms_bwd; kernel: "auto" or
     "plain"."""
     M, N, ld_h = _rows_ld(h, "h")
-    shape, dtype, device, owned = h.shape, h.dtype, h.device, []
+    shape, dtype, device = h.shape, h.dtype, h.device
     if grad_dtype is not _f32 and grad_dtype is not dtype:
         raise ValueError("grad_dtype must be float32 or h's dtype")
     ld_dy, ld_dh = _rows_like(dy, "dy", shape, dtype, device), _rows_like(dh, "dh", shape, dtype, device)
     _vec_like(gamma, "gamma", N, dtype, device)
     _vec_like(rstd, "rstd", M, _f32, device)
-    dx = _new(shape, dtype, device, owned) if dx is None else dx
+    dx = _empty(shape, dtype, device, stream) if dx is None else dx
     ld_dx = _rows_like(dx, "dx", shape, dtype, device)
     if dgamma is None:
-        dgamma = _grads(None, "dgamma", N, grad_dtype, device, accumulate)
-        owned.append(dgamma)
+        dgamma = _grads(None, "dgamma", N, grad_dtype, device, accumulate, stream)
     else:
         _vec_like(dgamma, "dgamma", N, grad_dtype, device)
     if workspace is None:
-        workspace = _new(max(bwd_workspace_bytes(M, N, dtype, False, device), 1), torch.uint8, device, owned)
+        workspace = _empty(max(bwd_workspace_bytes(M, N, dtype, False, device), 1), torch.uint8, device, stream)
     elif workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on h's device")
     opt = None
@@ -610,7 +620,7 @@ def rms_add_bwd(dy: torch.Tensor, dh: torch.Tensor, h: torch.Tensor, gamma: torc
                                       _ROW_KERNELS[kernel], 0, 0))
     _enqueue("rms_add_bwd", device, stream,
              (dy.data_ptr(), dh.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-              dgamma.data_ptr(), M, N, _code(h), workspace.data_ptr(), workspace.nbytes, ld_dh, opt), owned)
+              dgamma.data_ptr(), M, N, _code(h), workspace.data_ptr(), workspace.nbytes, ld_dh, opt))
     return dx, dgamma
 
 
@@ -690,20 +700,18 @@ def grad_workspace_bytes(device=None) -> int:
         return int(lib().gbn_grad_workspace_bytes())
 
 
-def _grad_args(grads, norm, workspace, owned):
+def _grad_args(grads, norm, workspace, stream):
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     device = grads.device
     if device is None:
         device = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        owned.append(norm)
+        norm = _empty((), _f32, device, stream)
     else:
         _vec_like(norm, "norm", 1, _f32, device)
     if workspace is None:
-        workspace = torch.empty(grad_workspace_bytes(device), dtype=torch.uint8, device=device)
-        owned.append(workspace)
+        workspace = _empty(grad_workspace_bytes(device), torch.uint8, device, stream)
     elif workspace.get_device() != device.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the gradients' device")
     return grads, norm, workspace, device
@@ -713,10 +721,9 @@ def grad_norm(grads, *, norm: Optional[torch.Tensor] = None, workspace=None, str
     """The 2-norm of all gradients together, as a float32 tensor of no dimensions.
 
     grads: a GradList, or tensors (a GradList is made for the call)."""
-    owned = []
-    grads, norm, workspace, device = _grad_args(grads, norm, workspace, owned)
+    grads, norm, workspace, device = _grad_args(grads, norm, workspace, stream)
     _enqueue("gbn_grad_norm", device, stream,
-             (grads._table, len(grads.tensors), norm.data_ptr(), workspace.data_ptr(), workspace.nbytes), owned)
+             (grads._table, len(grads.tensors), norm.data_ptr(), workspace.data_ptr(), workspace.nbytes))
     return norm
 
 
@@ -728,8 +735,7 @@ def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: Opti
     grads: a GradList, or tensors (a GradList is made for the call); they are
     clipped in place, or into ``out`` (a GradList or tensors of the same
     shapes, types and layouts)."""
-    owned = []
-    grads, norm, workspace, device = _grad_args(grads, norm, workspace, owned)
+    grads, norm, workspace, device = _grad_args(grads, norm, workspace, stream)
     grads._check_apart()
     if out is not None:
         if not isinstance(out, GradList):
@@ -737,7 +743,7 @@ def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, out=None, norm: Opti
         out._check_out_of(grads)
     _enqueue("gbn_grad_clip", device, stream,
              (grads._table, None if out is None else out._table, len(grads.tensors), max_norm, eps, norm.data_ptr(),
-              workspace.data_ptr(), workspace.nbytes), owned)
+              workspace.data_ptr(), workspace.nbytes))
     return norm
 
 
@@ -780,10 +786,10 @@ def _host_args(fn, dy, x, gamma, stats, dx, grads):
     return M, N, dx, out
 
 
-def _host_workspace(workspace, M, N, dtype, ln, device, chunk_rows):
+def _host_workspace(workspace, M, N, dtype, ln, device, chunk_rows, stream):
     need = bwd_host_workspace_bytes(M, N, dtype, ln, device, chunk_rows)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        workspace = _new(torch.empty, max(need, 1), dtype=torch.uint8, device=device, stream=stream)
     if workspace.device != torch.device(device) or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a device buffer of at least {need} bytes")
     return workspace, workspace.numel() * workspace.element_size()
@@ -798,7 +804,7 @@ def ln_bwd_host(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: to
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     M, N, dx, (dgamma, dbeta) = _host_args("ln_bwd_host", dy, x, gamma, (("mean", mean), ("rstd", rstd)), dx,
                                            (("dgamma", dgamma), ("dbeta", dbeta)))
-    workspace, wsb = _host_workspace(workspace, M, N, x.dtype, True, device, chunk_rows)
+    workspace, wsb = _host_workspace(workspace, M, N, x.dtype, True, device, chunk_rows, stream)
     opt = _host_options(chunk_rows)
     with torch.cuda.device(device):
         _check("ln_bwd_host", lib().ln_bwd_host_ex(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
@@ -815,7 +821,7 @@ def rms_bwd_host(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, rstd: t
     is.  chunk_rows as for ln_bwd_host."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     M, N, dx, (dgamma,) = _host_args("rms_bwd_host", dy, x, gamma, (("rstd", rstd),), dx, (("dgamma", dgamma),))
-    workspace, wsb = _host_workspace(workspace, M, N, x.dtype, False, device, chunk_rows)
+    workspace, wsb = _host_workspace(workspace, M, N, x.dtype, False, device, chunk_rows, stream)
     opt = _host_options(chunk_rows)
     with torch.cuda.device(device):
         _check("rms_bwd_host", lib().rms_bwd_host_ex(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(rstd), _ptr(dx),
@@ -840,7 +846,7 @@ def _act_host(fn: str, dy: torch.Tensor, preact: torch.Tensor, dx, workspace, de
     with torch.cuda.device(device):
         need = int(lib().gbn_act_host_workspace_bytes_ex(dy.numel(), code, ctypes.byref(opt)))
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+            workspace = _new(torch.empty, max(need, 1), dtype=torch.uint8, device=device, stream=stream)
         wsb = workspace.numel() * workspace.element_size()
         if workspace.device != device or wsb < need:
             raise ValueError(f"{fn}: workspace must be a device buffer of at least {need} bytes")
