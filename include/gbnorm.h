@@ -399,9 +399,14 @@ int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y,
  *   code = round(v * (Q/a)),  scale = rstd * a * (1/Q):  code * scale stands
  *   for y = gamma * h * rstd.
  * Q/a, its product with v, 1/Q and the scale's two products are float32
- * operations, rounded to nearest even, and so is the code.  A row (group) of zeros has codes 0 and
- * scale 0; where a row holds a NaN or an infinity, scales and e4m3 codes
- * are NaN as y would be (int8 codes of a NaN are 0).
+ * operations, rounded to nearest even, and so is the code.  A row (group) of
+ * zeros has codes 0 and scale 0, with eps = 0 too.  A NaN in a row makes all of
+ * the row's scales NaN (those of groups of zeros too), and the e4m3 codes of the
+ * row (group) that it stands in.  An infinity leaves rstd 0; the scale of the
+ * row (group) that it stands in is NaN, its own e4m3 code too, and the finite
+ * elements' codes there are 0; the row's other groups have their codes and scale
+ * 0, as y is 0 there.  int8 codes are 0 where e4m3's are NaN.  Finite values
+ * whose squares' sum is above float32's range leave rstd and scales 0.
  *   q [M,N] one byte each (out); scale [M] f32 (group 0) or
  *   [M, ceil(N/128)] f32, contiguous (out); h [M,N] dtype (out); rstd [M] f32
  *   (out); strides, kernel and overlaps as for rms_add_fwd (q overlaps no

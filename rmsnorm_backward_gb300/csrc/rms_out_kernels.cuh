@@ -68,8 +68,10 @@ __device__ __forceinline__ float quant_factor(float a) {
     if (a == 0.f) return 0.f;
     return quant_top<KIND>() / (quant_tiny(a) ? a * kRaise : a);
 }
+// (eps = 0 leaves a row of zeros an infinite rstd, whose product with 0 were NaN)
 template <int KIND>
 __device__ __forceinline__ float quant_scale(float rstd, float a) {
+    if (a == 0.f && rstd > 3.402823466e38f) return 0.f;
     return rstd * a * (1.f / quant_top<KIND>());
 }
 
