@@ -83,16 +83,56 @@ __device__ __forceinline__ void add(Pair &p, const Pair &q) {
     add(p, q.hi);
     p.lo += q.lo;
 }
+__device__ __forceinline__ Pair pair_of(float hi, float lo) {
+    Pair p;
+    p.hi = hi, p.lo = lo;
+    return p;
+}
+// its value; of an infinite or NaN sum what was lost means nothing
+__device__ __forceinline__ double value(const Pair &p) {
+    return static_cast<double>(p.hi) + (fabsf(p.hi) <= 3.402823466e38f ? static_cast<double>(p.lo) : 0.0);
+}
 
-// A thread's sums of squares: of x, of x * 2^-80 where a batch's sum is above
-// 2^60 (or not finite), of x * 2^80 where it is below 2^-80.  Squares from
-// there on are normal float32 values or negligible in their batch, and the
-// sums stay in range for 2^34 batches.
+// A thread's sums of squares, pairs each: of x, of x * 2^-80 where a batch's sum
+// is above 2^60 (or not finite), of x * 2^80 where it is below 2^-80.  Squares
+// from there on are normal float32 values, exact multiples of 2^-138 or
+// negligible in their batch, and the sums stay in range for 2^34 batches.
 constexpr float kBatchMost = 0x1p60f, kBatchLeast = 0x1p-80f;
 struct Sums {
-    Pair mid;
-    float big = 0.f, small = 0.f;
+    Pair mid, big, small;
+    __device__ __forceinline__ bool scaled() const { return big.hi != 0.f || small.hi != 0.f; }
 };
+
+__device__ __forceinline__ GradSums sums_out(const Sums &s) {
+    return GradSums{s.mid.hi, s.mid.lo, s.big.hi, s.small.hi, s.big.lo, s.small.lo};
+}
+// Adds the GradSums at from, from + step, ... below to: the ordinary sums first,
+// four loads at a time, then the scaled ones where there are any (a
+// branch at each made 1 us of a clip).
+template <bool GLOBAL>
+__device__ __forceinline__ void sums_in(Sums &s, const GradSums *from, const GradSums *to, int step) {
+    auto half = [](const GradSums *p, int i) {
+        const float4 *at = reinterpret_cast<const float4 *>(p) + i;
+        return GLOBAL ? __ldcg(at) : *at;
+    };
+    bool scaled = false;
+    for (const GradSums *p = from; p < to; p += 4 * step) {
+        float4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = p + i * step < to ? half(p + i * step, 0) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            add(s.mid, pair_of(q[i].x, q[i].y));
+            scaled |= q[i].z != 0.f || q[i].w != 0.f;
+        }
+    }
+    if (!scaled) return;
+    for (const GradSums *p = from; p < to; p += step) {
+        const float4 q = half(p, 0), r = half(p, 1);
+        add(s.big, pair_of(q.z, r.x));
+        add(s.small, pair_of(q.w, r.y));
+    }
+}
 
 template <typename T>
 __device__ __forceinline__ float sum_squares(const uint4 (&raw)[4], float scale) {
@@ -113,10 +153,12 @@ __device__ __forceinline__ float sum_squares(const uint4 (&raw)[4], float scale)
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// p and a batch's squares, scaled
 template <typename T>
-__device__ __noinline__ float scaled_squares(uint4 v0, uint4 v1, uint4 v2, uint4 v3, float scale) {
+__device__ __noinline__ Pair scaled_squares(Pair p, uint4 v0, uint4 v1, uint4 v2, uint4 v3, float scale) {
     const uint4 raw[4] = {v0, v1, v2, v3};
-    return sum_squares<T>(raw, scale);
+    add(p, sum_squares<T>(raw, scale));
+    return p;
 }
 
 template <typename T>
@@ -128,9 +170,9 @@ __device__ __forceinline__ void add_batch(Sums &sums, const uint4 (&raw)[4]) {
         uint32_t any = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) any |= raw[j].x | raw[j].y | raw[j].z | raw[j].w;
-        if (any) sums.small += scaled_squares<T>(raw[0], raw[1], raw[2], raw[3], 0x1p80f);
+        if (any) sums.small = scaled_squares<T>(sums.small, raw[0], raw[1], raw[2], raw[3], 0x1p80f);
     } else {
-        sums.big += scaled_squares<T>(raw[0], raw[1], raw[2], raw[3], 0x1p-80f);
+        sums.big = scaled_squares<T>(sums.big, raw[0], raw[1], raw[2], raw[3], 0x1p-80f);
     }
 }
 
@@ -139,9 +181,9 @@ __device__ __forceinline__ void add_one(Sums &sums, float f) {
     if (b >= kBatchLeast && b <= kBatchMost)
         add(sums.mid, b);
     else if (b < kBatchLeast)
-        sums.small += (f * 0x1p80f) * (f * 0x1p80f);
+        add(sums.small, (f * 0x1p80f) * (f * 0x1p80f));
     else
-        sums.big += (f * 0x1p-80f) * (f * 0x1p-80f);
+        add(sums.big, (f * 0x1p-80f) * (f * 0x1p-80f));
 }
 
 template <typename T>
@@ -168,29 +210,29 @@ __device__ __forceinline__ void add_chunk(Sums &sums, const GradEntry &t, uint32
     for (int j = 0; j < kGradVecs / 4; ++j) add_batch<T>(sums, raw[j]);
 }
 
-// The CTA's sums in a fixed order, on every thread; sm holds 4 floats a warp.
-__device__ __forceinline__ Sums cta_sum(Sums v, float4 *sm) {
+__device__ __forceinline__ Pair shuffled(const Pair &p, int o) {
+    Pair q;
+    q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
+    q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
+    return q;
+}
+
+// The CTA's sums in a fixed order, on every thread; sm holds a GradSums a warp.
+// The scaled sums are looked at where there are any.
+__device__ __forceinline__ Sums cta_sum(Sums v, GradSums *sm) {
+    const bool scaled = __any_sync(0xffffffffu, v.scaled());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        Pair q;
-        q.hi = __shfl_xor_sync(0xffffffffu, v.mid.hi, o);
-        q.lo = __shfl_xor_sync(0xffffffffu, v.mid.lo, o);
-        add(v.mid, q);
-        v.big += __shfl_xor_sync(0xffffffffu, v.big, o);
-        v.small += __shfl_xor_sync(0xffffffffu, v.small, o);
+        add(v.mid, shuffled(v.mid, o));
+        if (scaled) {
+            add(v.big, shuffled(v.big, o));
+            add(v.small, shuffled(v.small, o));
+        }
     }
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float4(v.mid.hi, v.mid.lo, v.big, v.small);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = sums_out(v);
     __syncthreads();
     Sums s;
-#pragma unroll
-    for (int w = 0; w < kGradThreads / 32; ++w) {
-        const float4 q = sm[w];
-        Pair m;
-        m.hi = q.x, m.lo = q.y;
-        add(s.mid, m);
-        s.big += q.z;
-        s.small += q.w;
-    }
+    sums_in<false>(s, sm, sm + kGradThreads / 32, 1);
     __syncthreads();
     return s;
 }
@@ -219,15 +261,14 @@ __device__ __forceinline__ int find_entry(const GradTable<CAP> &t, uint32_t c) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ float4 sm[kGradThreads / 32];
+    __shared__ GradSums sm[kGradThreads / 32];
     // the gradients, and whoever still reads the partial sums, come before
     // this kernel on the stream; the clip may launch meanwhile and waits
     griddep_wait();
     griddep_launch_dependents();
     Sums sums;
     if (t.add && threadIdx.x == 0) {  // a later launch of the same list
-        const GradSums p = t.partial[blockIdx.x];
-        sums.mid.hi = p.hi, sums.mid.lo = p.lo, sums.big = p.big, sums.small = p.small;
+        sums_in<true>(sums, t.partial + blockIdx.x, t.partial + blockIdx.x + 1, 1);
     }
     uint32_t c, c1;
     cta_range(t.chunks, c, c1);
@@ -246,36 +287,28 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_norm_kernel
         }
     }
     sums = cta_sum(sums, sm);
-    if (threadIdx.x == 0) t.partial[blockIdx.x] = GradSums{sums.mid.hi, sums.mid.lo, sums.big, sums.small};
+    if (threadIdx.x == 0) t.partial[blockIdx.x] = sums_out(sums);
 }
 
 // The norm from the CTAs' sums, in a fixed order: the float32 root of the
 // pair, improved by one step of Newton's method from the pair's residual, or
 // a float64 root where some batches were scaled or the sum is zero, infinite
 // or NaN (a norm above the largest float32 is infinite).
-__device__ __forceinline__ float norm_of(const GradSums *partial, int total, float4 *sm) {
+__device__ __forceinline__ float norm_of(const GradSums *partial, int total, GradSums *sm) {
     Sums v;
-    for (int i = threadIdx.x; i < total; i += kGradThreads) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(partial + i));
-        Pair m;
-        m.hi = q.x, m.lo = q.y;
-        add(v.mid, m);
-        v.big += q.z;
-        v.small += q.w;
-    }
+    sums_in<true>(v, partial + threadIdx.x, partial + total, kGradThreads);
     v = cta_sum(v, sm);
-    if (v.big == 0.f && v.small == 0.f && v.mid.hi >= 0x1p-100f && v.mid.hi <= 0x1p120f) {
+    if (!v.scaled() && v.mid.hi >= 0x1p-100f && v.mid.hi <= 0x1p120f) {
         const float r = sqrtf(v.mid.hi);
         return r + (fmaf(-r, r, v.mid.hi) + v.mid.lo) / (2.f * r);
     }
-    const double d = static_cast<double>(v.mid.hi) + static_cast<double>(v.mid.lo) +
-                     static_cast<double>(v.big) * 0x1p160 + static_cast<double>(v.small) * 0x1p-160;
+    const double d = value(v.mid) + value(v.big) * 0x1p160 + value(v.small) * 0x1p-160;
     return static_cast<float>(sqrt(d));
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_norm_finish_kernel(const GradSums *partial, int total,
                                                                        float *norm) {
-    __shared__ float4 sm[kGradThreads / 32];
+    __shared__ GradSums sm[kGradThreads / 32];
     griddep_wait();
     const float n = norm_of(partial, total, sm);
     if (threadIdx.x == 0) *norm = n;
@@ -327,7 +360,7 @@ __device__ __forceinline__ void scale_chunk(const GradEntry &t, uint32_t chunk, 
 
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradCtasPerSm) grad_clip_kernel(const __grid_constant__ GradTable<CAP> t) {
-    __shared__ float4 sm[kGradThreads / 32];
+    __shared__ GradSums sm[kGradThreads / 32];
     griddep_wait();
     const float norm = norm_of(t.partial, t.total, sm);
     if (blockIdx.x == 0 && threadIdx.x == 0 && !t.add) *t.norm = norm;

@@ -15,9 +15,10 @@ constexpr int kGradVecs = 8;                                 // 16-byte vectors 
 constexpr int kGradChunkVecs = kGradThreads * kGradVecs;     // 32 KiB
 constexpr int kGradCtasPerSm = 4;
 
-// a CTA's sums of squares: a float32 pair, and those scaled by 2^-160 and 2^160
+// a CTA's sums of squares, float32 pairs each: ordinary ones, and those scaled
+// by 2^-160 (big) and 2^160 (small)
 struct alignas(16) GradSums {
-    float hi, lo, big, small;
+    float hi, lo, big, small, big_lo, small_lo;
 };
 
 // CTAs for `chunks` chunks in all; the workspace has a GradSums for each
