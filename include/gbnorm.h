@@ -383,8 +383,8 @@ int gelu_bwd_host_ex(const void *dy, const void *preact, void *dx, int64_t n, in
  *   rstd [M] f32 (out).  ld_x, ld_res, ld_y, ld_h: row strides in elements,
  *   0 for N, else >= N.  kernel: GBN_KERNEL_AUTO or GBN_KERNEL_PLAIN.
  * y and h may each be x or residual (the same pointer and stride: the
- * residual stream updated in place); any other overlap of an output with a
- * row of another tensor is GBN_EINVAL.  M = 0 is a no-op.
+ * residual stream updated in place); any other overlap of an output (rstd
+ * too) with a row of another tensor or with gamma is GBN_EINVAL.  M = 0 is a no-op.
  */
 int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y, void *h, float *rstd, float eps,
                 int64_t M, int64_t N, int dtype, int64_t ld_x, int64_t ld_res, int64_t ld_y, int64_t ld_h, int kernel,
@@ -409,8 +409,8 @@ int rms_add_fwd(const void *x, const void *residual, const void *gamma, void *y,
  * whose squares' sum is above float32's range leave rstd and scales 0.
  *   q [M,N] one byte each (out); scale [M] f32 (group 0) or
  *   [M, ceil(N/128)] f32, contiguous (out); h [M,N] dtype (out); rstd [M] f32
- *   (out); strides, kernel and overlaps as for rms_add_fwd (q overlaps no
- *   other tensor).
+ *   (out); strides, kernel and overlaps as for rms_add_fwd (q and scale overlap
+ *   no other tensor).
  */
 enum { GBN_E4M3 = 16, GBN_INT8 = 17 };
 int rms_fwd_q8(const void *x, const void *gamma, void *q, float *scale, float *rstd, float eps, int64_t M, int64_t N,
@@ -428,7 +428,7 @@ int rms_add_fwd_q8(const void *x, const void *residual, const void *gamma, void 
  * in float32 before the one rounding to dtype.
  *   dy, dh, h [M,N] dtype (in), gamma [N] (in), rstd [M] f32 (in, required),
  *   dx [M,N] dtype (out; may be dy, dh or h: same pointer and stride, any
- *   other overlap is GBN_EINVAL), dgamma [N] (out).  ld_dh: row stride of dh
+ *   other overlap with a tensor of the call is GBN_EINVAL), dgamma [N] (out).  ld_dh: row stride of dh
  *   (0: N).  Of opt (may be NULL) ld_x (of h), ld_dy, ld_out (of dx),
  *   accumulate, grad_dtype, kernel and wait_limit_ns apply; the others must
  *   be zero.  workspace: gbn_bwd_workspace_bytes(M, N, dtype, 0) bytes, as for

@@ -679,6 +679,20 @@ bool apart(const RowSpan &a, const RowSpan &b, int64_t M) {
 // an output against an input row by row: apart, or the same rows (updated in place)
 bool out_over_in(const RowSpan &out, const RowSpan &in, int64_t M) { return same_rows(out, in) || apart(out, in, M); }
 
+// Whether the block of `bytes` at p (statistics, scales, gamma) has no byte in
+// common with the rows of a; between two rows it may lie.
+bool clear_of(const void *p, int64_t bytes, const RowSpan &a, int64_t M) {
+    if (!p || !a.p || bytes <= 0 || M <= 0) return true;
+    const intptr_t lo = reinterpret_cast<intptr_t>(p), row0 = reinterpret_cast<intptr_t>(a.p);
+    if (lo + bytes <= row0 || row0 + (M - 1) * a.ld + a.row <= lo) return true;
+    if (lo < row0) return false;
+    const intptr_t into = (lo - row0) % a.ld;  // from the start of the row before it
+    return into >= a.row && into + bytes <= a.ld;
+}
+bool blocks_apart(const void *p, int64_t p_bytes, const void *q, int64_t q_bytes) {
+    return clear_of(p, p_bytes, RowSpan{q, q_bytes, q_bytes}, 1);
+}
+
 // whether every address is a multiple of the element (null ones are told apart elsewhere)
 template <typename... P>
 bool element_aligned(int64_t es, P... q) {
@@ -868,6 +882,13 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
         if (kind == kOutSame ? !out_over_in(so, sr, M) : !apart(so, sr, M)) return GBN_EINVAL;
         if (!apart(so, sh, M) || !out_over_in(sh, sx, M) || !out_over_in(sh, sr, M)) return GBN_EINVAL;
     }
+    const int64_t stats = 4 * M, scales = kind == kOutSame ? 0 : group ? stats * ((N + kQuantGroup - 1) / kQuantGroup) : stats;
+    if (!blocks_apart(rstd, stats, gamma, N * es) || !blocks_apart(scale, scales, gamma, N * es) ||
+        !blocks_apart(scale, scales, rstd, stats) || !clear_of(gamma, N * es, so, M))
+        return GBN_EINVAL;
+    for (const RowSpan &rows : {sx, so, has_res ? sr : sx, has_res ? sh : sx})
+        if (!clear_of(rstd, stats, rows, M) || !clear_of(scale, scales, rows, M)) return GBN_EINVAL;
+    if (has_res && !clear_of(gamma, N * es, sh, M)) return GBN_EINVAL;
     DevInfo d;
     if ((st = device_info(&d)) != GBN_OK) return st;
     OutParams p{};
@@ -947,6 +968,9 @@ int rms_add_bwd_impl(const void *dy, const void *dh, const void *h, const void *
         const RowSpan sdx{dx, o.ld_out * es, N * es}, sdy{dy, o.ld_dy * es, N * es}, sdh{dh, ld_dh * es, N * es},
             sh{h, o.ld_x * es, N * es};
         if (!out_over_in(sdx, sdy, M) || !out_over_in(sdx, sdh, M) || !out_over_in(sdx, sh, M)) return GBN_EINVAL;
+        if (!clear_of(gamma, N * es, sdx, M) || !clear_of(rstd, 4 * M, sdx, M) ||
+            !clear_of(dgamma, N * elem_bytes(o.grad_dtype), sdx, M))
+            return GBN_EINVAL;
         DevInfo d;
         if ((st = device_info(&d)) != GBN_OK) return st;
         if (workspace_bytes_given < workspace_bytes(M, N, false, d)) return GBN_EWORKSPACE;
