@@ -456,7 +456,8 @@ int rms_add_bwd(const void *dy, const void *dh, const void *h, const void *gamma
  *   gbn_grad_clip: out is NULL (in place) or `count` descriptors of the same
  *   n and dtype, none of which overlaps a gradient other than its own and
  *   that one not in part.  A tensor must not be listed twice.  A norm that is
- *   NaN makes every output NaN, an infinite one makes finite elements zero.
+ *   NaN makes every output NaN, an infinite one makes finite elements zero (NaN
+ *   where max_norm is infinite too: the quotient is).
  *   max_norm >= 0, eps >= 0, neither NaN.
  * gbn_grad_check returns GBN_EINVAL if two of the tensors share memory (or a
  * descriptor is invalid); it needs no device.

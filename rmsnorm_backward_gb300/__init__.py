@@ -12,6 +12,11 @@ Names follow the pages' notation: ``ln_fwd``, ``rms_fwd`` produce ``y`` and
 the per-row statistics (``mean``, ``rstd``); ``ln_bwd``, ``rms_bwd`` take
 ``dy`` and the saved statistics and produce ``dx``, ``dgamma`` (and
 ``dbeta``).
+
+``stream=`` (a torch stream or its handle) puts a call on another stream than
+the current one; what it allocates is that stream's.  The caller orders the
+streams that make its inputs and take its results, and keeps the inputs until
+it is done (or marks them with record_stream).
 """
 from __future__ import annotations
 
@@ -646,7 +651,9 @@ class GradList:
 
     Every tensor's elements have to fill one block of memory (contiguous, or a
     permutation of that).  The list keeps the tensors and their storages; it
-    describes the memory that they had when it was made."""
+    describes the memory that they had when it was made, so it is for
+    gradients that stay where they are: after zero_grad(set_to_none=True) the
+    parameters have others, which the list does not know of."""
 
     def __init__(self, tensors):
         tensors = list(tensors)

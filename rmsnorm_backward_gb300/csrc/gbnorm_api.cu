@@ -68,8 +68,11 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Number of row blocks (CTAs) G: one per SM, more only when a block would
 // exceed kMaxRowsPerCta rows.  It depends on (M, SM count) only, so the
-// workspace size and the column reduce's order do not depend on buffer
-// alignment or on the kernel that takes the rows.
+// workspace size does not depend on buffer alignment or on the kernel that
+// takes the rows, and neither does the column reduce's order in ln_bwd and
+// rms_bwd.  rms_add_bwd takes fewer blocks for rows across 16-byte boundaries
+// and for short ones (add_bwd_plan), so its dgamma may differ in the last bits
+// between alignments and kernels; it is the same from run to run.
 int grid_rows(int64_t M, const DevInfo &d) {
     if (M <= 0) return 0;
     int64_t G = d.sms;
@@ -896,7 +899,6 @@ int rms_out_impl(int kind, int64_t group, const void *x, const void *res, bool h
     p.rstd = rstd; p.scale = scale; p.eps = eps; p.M = M; p.N = static_cast<int>(N);
     p.ld_x = ld_x; p.ld_res = ld_res; p.ld_h = ld_h; p.ld_out = ld_out;
     p.kind = kind; p.group = group != 0 && N > kQuantGroup; p.err = d.err;  // one group is a row
-   
     if (kernel == GBN_KERNEL_AUTO) {
         const OutPlan P = out_plan(dtype, d, &p);
         if (P.short_rows) return cuda_status(launch_rms_out_short(dtype, P.vec, p, d.sms, stream));

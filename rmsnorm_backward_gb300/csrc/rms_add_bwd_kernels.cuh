@@ -24,8 +24,11 @@ namespace gbn {
 // block of rows.  First a warp to a row forms mean(dyhat*xhat); then the CTA
 // goes over the rows once for each slab of 8192 columns, a thread owning eight
 // of them and their dgamma sums in registers, so h and dy are read twice.
-// (Accumulating in global memory in one go, 256 threads a CTA, took 1808 us at
-// 16384x4096 bf16.)
+// For rows too wide for the ring (16384 elements of 16 bits, about 9650 of
+// float32, less where a CTA has many rows, whose rstd it keeps) and tensors whose
+// rows lie differently to 16-byte boundaries: 4096x20000 bf16 228 us, 2.9 TB/s,
+// 4096x12288 float32 191 us, 4.2 TB/s.  (Accumulating in global memory in one go, 256
+// threads a CTA, took 1808 us at 16384x4096 bf16.)
 // ---------------------------------------------------------------------------
 constexpr int kAddBwdPlainThreads = 1024, kAddBwdPlainCols = 8;
 

@@ -152,9 +152,11 @@ __device__ __forceinline__ uint8_t quant1(float a) {
 // any N, stride and alignment: one row at a time per CTA, scalar accesses.
 // A warp owns whole blocks of 128 columns (four columns 32 apart a lane), so
 // a group's maximum is a warp's; h is read again for the output, by the
-// threads that wrote it.  For rows too wide for the ring and tensors whose rows
-// lie differently to 16-byte boundaries (4096x20000 bf16 259 us, 2.5 TB/s: two
-// bytes to a load keep too little in flight).
+// threads that wrote it.  For rows too wide for the ring (its threads hold 16384
+// elements; two stages of a float32 row with its residual fit up to 14500) and
+// tensors whose rows lie differently to 16-byte boundaries (4096x20000 bf16 255
+// us, 2.6 TB/s, 2048x16384 float32 156 us, 3.4 TB/s: an element to a load keeps
+// too little in flight).
 // ---------------------------------------------------------------------------
 constexpr int kOutPlainThreads = 256;
 
@@ -276,11 +278,10 @@ cudaError_t rms_out_plain_dispatch(int kind, bool group, const OutParams &p, int
 // bf16 with the residual 81.7 us, 6.57 TB/s (98% of the measured copy rate);
 // to e4m3 by 128 columns, 8192x16384, 144 us, 6.5 TB/s.  Without the residual
 // there are fewer bytes to hide the work of a code behind: 16384x4096 bf16 to
-// e4m3 36 us, 5.6 TB/s, where the warps' instructions bound it: half the issue
-// slots are used, 4 warps a scheduler wait for one another's latencies.
-// Code counts even where it does not run: with and without a residual in one
-// kernel 46 us against 43 (by 128 columns), the copies of a tensor's end rows
-// inlined 79 against 67 (27711x2202 to int8).
+// e4m3 37 us, 5.4 TB/s, bound by the latencies of the warps' work: half the
+// issue slots are used, the 4 warps a scheduler that 128 registers allow are
+// too few to fill the others.  Code counts even where it does not run: with and
+// without a residual in one kernel 46 us against 43 (by 128 columns).
 //
 // How the rows lie (RowLie):
 //  * kLieFull: they start and end on 16 bytes (their codes on V) and are as
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) rms_out_ring_kernel(const OutP
     // a thread's vectors of a staged row (kLieShift)
     const bool whole_warp = (ts | 31) + 1 + (NV - 1) * tpr <= N / V;  // none of the warp's beyond the row
     auto shifted = [&](const unsigned char *row_at, uint4 *a) {
-by_words<V>(s, [&](auto o) {
+        by_words<V>(s, [&](auto o) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int v = min(ts + j * tpr, ve - 1);

@@ -70,3 +70,14 @@ def test_infinities_and_nan_among_scaled_batches(n):
         assert torch.isnan(gbn.grad_norm([t]))
     t = torch.full((n,), 3e38, device="cuda")  # the norm of n of them is no float32
     assert float(gbn.grad_norm([t])) == float("inf")
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 1.0, float("inf")])
+def test_an_infinite_norm(max_norm):
+    """Finite elements become zero, but where max_norm is infinite too: inf / inf is NaN, and so is every output."""
+    t = torch.ones(1000, device="cuda")
+    t[10] = float("inf")
+    assert float(gbn.grad_clip([t], max_norm)) == float("inf")
+    assert torch.isnan(t[10])
+    rest = torch.cat([t[:10], t[11:]])
+    assert torch.isnan(rest).all() if max_norm == float("inf") else (rest == 0).all()
